@@ -113,6 +113,107 @@ pkv_status paged_kv_zero_and_write(const void *k, const void *v,
                                    const pkv_cache *cache, const int32_t *block_ids,
                                    int64_t n, int ids_on_host, void *stream);
 
+/* A rotary embedding with positions on several axes (one for text; time,
+ * height and width for images and video).  The struct and its arrays are
+ * HOST memory, read during the call only. */
+#define PKV_ROPE_MAX_AXES 4
+#define PKV_ROPE_MAX_PAIRS 64
+typedef struct {
+    const double *frequencies; /* [rotary_dim / 2] radians per position,
+                                  finite, at most 1024 in magnitude       */
+    const uint8_t *axis;       /* [rotary_dim / 2] position axis of a pair */
+    int32_t num_axes;          /* 1 .. PKV_ROPE_MAX_AXES                   */
+    int32_t rotary_dim;        /* leading elements of a head that turn: a
+                                  multiple of 16, 16 .. head_dim           */
+    int32_t interleaved;       /* pair i is elements (i, i + rotary_dim / 2)
+                                  when 0, (2 i, 2 i + 1) otherwise         */
+} pkv_rope;
+
+/* Rotary positions and the slot-mapped write in one launch: pair i of every
+ * q and k head of token t turns by positions[axis[i]][t] * frequencies[i]
+ * radians, (x, y) -> (x cos a - y sin a, x sin a + y cos a); turned q goes
+ * to q_out, turned k and v to the token's slot as by paged_kv_write.  Source
+ * of the write: vLLM concept page (compassingai.com), "15 分钟专家深入" item
+ * 2; the pages do not describe positions.  Position and slot are separate,
+ * so a sequence whose slots moved (paged_kv_evict) keeps its positions.
+ *   q             bf16 [num_tokens, num_heads, head_dim]; rows of heads are
+ *                 contiguous, tokens q_stride elements apart, so that q, k
+ *                 and v may be slices of one projection's output.  May be
+ *                 NULL with num_heads 0 (k and v only).
+ *   k, v          bf16 [num_tokens, num_kv_heads, head_dim], likewise.
+ *   positions     int32 [num_axes, num_tokens], axes axis_stride elements
+ *                 apart; any value, negative ones included.
+ *   slot_mapping  as for paged_kv_write: a negative slot writes no k and v
+ *                 (q is turned all the same); a slot past the pool is a
+ *                 device range error (k and v of the token are skipped).
+ *   q_out         bf16, tokens q_out_stride elements apart; q itself (same
+ *                 stride) turns q in place, any other overlap with q, k or
+ *                 v is rejected.
+ * Strides are multiples of 8 elements and at least a row, pointers 16-byte
+ * aligned.  Angles are within 2^-25 of a turn at every position; the
+ * rotation is binary32 and rounded once, to bf16 or (k and v of an fp8
+ * cache) to E4M3 of x / scale as by paged_kv_write.  Elements past
+ * rotary_dim, and v, keep their bits in q_out and in a bf16 cache. */
+pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const void *k,
+                               int64_t k_stride, const void *v, int64_t v_stride,
+                               const int32_t *positions, int64_t axis_stride,
+                               const int64_t *slot_mapping, int64_t num_tokens,
+                               int32_t num_heads, const pkv_rope *rope,
+                               const pkv_cache *cache, void *q_out,
+                               int64_t q_out_stride, void *stream);
+
+/* Eviction by accumulated attention weight: each sequence keeps
+ * n = min(seq_lens[b], keep[b]) tokens, which move together, in order, to
+ * positions 0 .. n - 1.  The pages describe only whole sequences leaving
+ * the cache (vLLM concept page, compassingai.com, "15 分钟专家深入" item 1);
+ * keeping part of one is this library's.  Kept are the last min(recent, n)
+ * tokens, the first min(sink, what is left of n), and of the others those
+ * with the largest weight: of equal weights the lower position, NaN below
+ * every number, -0 equal to +0.
+ *   weights       fp32 [batch, num_kv_heads, weights_stride]: token t's
+ *                 accumulated weight for t < seq_lens[b] (<= weights_stride),
+ *                 as kept by paged_attention_decode_weights.
+ *   keep          int32 [batch] (device), at least 0; max_keep bounds every
+ *                 n on the host.
+ *   per_head      non-zero: every kv head chooses by its own weights; zero:
+ *                 all heads keep the same tokens, chosen by the heads' sum
+ *                 (added in binary64, rounded once to binary32).
+ *   dst_tables    NULL: in place (the sequence's blocks must then be its
+ *                 own, shared with no other sequence); otherwise int32
+ *                 [batch, dst_max_blocks]: position i goes to row i % 16 of
+ *                 block dst_tables[b][i / 16], and the blocks read stay as
+ *                 they are.  No destination block may be read or written by
+ *                 another sequence of the call.
+ *   dst_weights   NULL: weights move in place; otherwise fp32 [batch,
+ *                 num_kv_heads, dst_weights_stride], not overlapping
+ *                 weights.
+ *   new_seq_lens  int32 [batch]: n; may be seq_lens itself.
+ *   kept          NULL or int32 [batch, per_head ? num_kv_heads : 1,
+ *                 max_keep]: the old positions of the kept tokens, -1 past n.
+ *   workspace     at least paged_kv_evict_workspace_bytes(...), 256-byte
+ *                 aligned.
+ * Weights at positions n .. seq_lens[b] - 1 become 0 (a later token starts
+ * there from 0); K and V rows past n, and weights past the old length, are
+ * left as they were.  A sequence with a negative length or keep, a length
+ * past its table or weights row, or n past max_keep, dst_tables or
+ * dst_weights is a device range error and is left alone (new_seq_lens[b] =
+ * seq_lens[b], kept -1); a row whose block lies outside the pool is
+ * reported and not moved. */
+pkv_status paged_kv_evict(const pkv_cache *cache, const int32_t *block_tables,
+                          int32_t max_blocks, const int32_t *seq_lens,
+                          float *weights, int64_t weights_stride,
+                          const int32_t *keep, int32_t batch, int32_t max_keep,
+                          int32_t sink, int32_t recent, int per_head,
+                          const int32_t *dst_tables, int32_t dst_max_blocks,
+                          float *dst_weights, int64_t dst_weights_stride,
+                          int32_t *new_seq_lens, int32_t *kept, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace paged_kv_evict needs (0 on invalid arguments).
+ * Host-only. */
+size_t paged_kv_evict_workspace_bytes(int32_t batch, int32_t num_kv_heads,
+                                      int64_t weights_stride, int32_t max_keep);
+
 /* Copy whole blocks: for each i, every byte of key_cache[dst_ids[i]] and
  * value_cache[dst_ids[i]] becomes the byte of block src_ids[i].  Source:
  * vLLM internals (naphjohn.github.io), §1.1 (copy-on-write of a shared
@@ -260,6 +361,47 @@ pkv_status paged_attention_decode_step(const void *q, const void *k_new,
                                        int32_t partition_tokens,
                                        void *workspace, size_t workspace_bytes,
                                        void *stream);
+
+/* Decode attention that also keeps each cached token's running attention
+ * weight, the measure paged_kv_evict goes by:
+ *   weights[b][kvh][t] = decay * weights[b][kvh][t]
+ *                        + sum over kv head kvh's query heads h of
+ *                          softmax(scale * q_h . K)[t],   t < seq_lens[b].
+ * Source of the attention: vLLM concept page (compassingai.com),
+ * "技术原理" pseudocode; the running weights are this library's.
+ *   k_new, v_new, new_start_loc, num_new_tokens  all NULL / 0, or the new
+ *                 tokens of a decode step, written first as by
+ *                 paged_attention_decode_step; the weights of positions
+ *                 written by the call start from 0 whatever they held.
+ *   weights       fp32 [batch, num_kv_heads, weights_stride] (device),
+ *                 weights_stride >= max_seq_len; entries at or past
+ *                 seq_lens[b] are left as they were.
+ *   decay         finite; 0 stores the step's weights without reading the
+ *                 old ones.
+ *   workspace     at least paged_attention_decode_weights_workspace_bytes(...)
+ *                 for the same arguments, 256-byte aligned: the split-KV
+ *                 partials and the step's scores.
+ * Other arguments, device range errors and the output (bit for bit) as for
+ * paged_attention_decode, or paged_attention_decode_step with new tokens.
+ * Weights are binary32 sums in a fixed order; a token excluded from the
+ * softmax (its block outside the pool, its wait timed out) gains 0.  A NaN
+ * score (NaN or opposing infinities in q or in a cached key of the sequence)
+ * makes its row of out and its kv head's weights NaN, as the formula does;
+ * paged_attention_decode may write 0 there. */
+pkv_status paged_attention_decode_weights(
+    const void *q, const void *k_new, const void *v_new,
+    const int32_t *new_start_loc, int64_t num_new_tokens,
+    const pkv_cache *cache, const int32_t *block_tables, int32_t max_blocks,
+    const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale,
+    void *out, float *weights, int64_t weights_stride, float decay,
+    int32_t max_seq_len, int32_t partition_tokens, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace paged_attention_decode_weights needs (0 on invalid
+ * arguments).  Host-only. */
+size_t paged_attention_decode_weights_workspace_bytes(
+    int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t max_seq_len, int32_t partition_tokens);
 
 /* Prefill / chunked-prefill attention over a paged cache: several query
  * tokens per sequence, causal within the sequence.  Source: vLLM concept

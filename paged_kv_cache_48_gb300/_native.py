@@ -38,6 +38,17 @@ class PkvCache(ctypes.Structure):
     ]
 
 
+class PkvRope(ctypes.Structure):
+    """Mirror of ``pkv_rope``."""
+    _fields_ = [
+        ("frequencies", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+        ("num_axes", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _SIGNATURES = {
     "paged_kv_write": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64,
@@ -88,6 +99,26 @@ _SIGNATURES = {
     "paged_attention_partition_tokens": (ctypes.c_int32, [
         ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_int32]),
+    "paged_kv_rope_write": (ctypes.c_int, [
+        _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+        ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int32,
+        ctypes.POINTER(PkvRope), ctypes.POINTER(PkvCache), _P, ctypes.c_int64,
+        _P]),
+    "paged_attention_decode_weights": (ctypes.c_int, [
+        _P, _P, _P, _P, ctypes.c_int64, ctypes.POINTER(PkvCache), _P,
+        ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P,
+        _P, ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
+        _P, ctypes.c_size_t, _P]),
+    "paged_attention_decode_weights_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32, ctypes.c_int32]),
+    "paged_kv_evict": (ctypes.c_int, [
+        ctypes.POINTER(PkvCache), _P, ctypes.c_int32, _P, _P, ctypes.c_int64,
+        _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int, _P, ctypes.c_int32, _P, ctypes.c_int64, _P, _P, _P,
+        ctypes.c_size_t, _P]),
+    "paged_kv_evict_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]),
     "pkv_check": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_int64)]),
     "pkv_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "pkv_version": (ctypes.c_int32, []),

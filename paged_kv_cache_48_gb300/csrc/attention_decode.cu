@@ -111,6 +111,17 @@ struct DecodeParams {
   long long num_new;
   uint8_t *k_cache, *v_cache;
   float k_scale;
+  // Running attention weights (kernels with WEIGHTS): every score (log2
+  // units, -inf where excluded) is kept in logits, unit (b, kv head, query
+  // sub-group) by unit, [logit_tokens][logit_heads] each, until the row's
+  // softmax statistics are known; weights_accumulate_kernel then adds the
+  // weights to weights [B, Hkv, weights_stride].
+  float *logits;
+  float *weights;
+  long long weights_stride;
+  int32_t logit_tokens;  // max_seq_len rounded up to whole blocks
+  int32_t logit_heads;   // heads of a sub-group, rounded up to an even count
+  float decay;
 };
 
 // First token of sequence b this launch attends to (0, or its group's
@@ -320,11 +331,22 @@ __device__ __forceinline__ void block_scores(uint32_t sk,
   for (int i = 0; i < 4; ++i) sc[i] = sa[i] + sb[i];
 }
 
+// WEIGHTS kernels: a block's 16 scores of heads 2c, 2c+1 (this lane's tokens
+// g and g + 8) to its [16][heads] piece of the unit's kept scores.
+__device__ __forceinline__ void keep_scores(float *lg, int heads, int g, int c, float s0, float s1,
+                                            float s2, float s3) {
+  if (2 * c < heads) {
+    *reinterpret_cast<float2 *>(lg + g * heads + 2 * c) = make_float2(s0, s1);
+    *reinterpret_cast<float2 *>(lg + (g + 8) * heads + 2 * c) = make_float2(s2, s3);
+  }
+}
+
 // Online softmax update with one block's scores and P.V accumulation; sv is
 // the shared address of the V tile, nv the block's valid tokens (0..16).
-template <bool FP8, int D, bool FULL>
+template <bool FP8, int D, bool FULL, bool WEIGHTS>
 __device__ __forceinline__ void block_update(uint32_t sv, int nv, const float (&sc)[4],
                                              float scale_log2, WarpState<FP8, D> &st, int lane,
+                                             float *lg, int lg_heads,
                                              uint32_t box_stride = 16 * Cfg<FP8, D>::BOX_BYTES) {
   using C = Cfg<FP8, D>;
   const int g = lane >> 2, c = lane & 3;
@@ -340,6 +362,7 @@ __device__ __forceinline__ void block_update(uint32_t sv, int nv, const float (&
   const float s1 = v_lo ? sc[1] * scale_log2 : -INFINITY;
   const float s2 = v_hi ? sc[2] * scale_log2 : -INFINITY;
   const float s3 = v_hi ? sc[3] * scale_log2 : -INFINITY;
+  if constexpr (WEIGHTS) keep_scores(lg, lg_heads, g, c, s0, s1, s2, s3);
   float bm0 = fmaxf(s0, s2), bm1 = fmaxf(s1, s3);
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
@@ -416,27 +439,28 @@ __device__ __forceinline__ void block_update(uint32_t sv, int nv, const float (&
 }
 
 // One 16-token block: scores, online softmax update and P.V accumulation.
-template <bool FP8, int D>
+template <bool FP8, int D, bool WEIGHTS>
 __device__ __forceinline__ void attend_block(uint32_t sk, uint32_t sv, int nv,
                                              const uint32_t (&qf)[Cfg<FP8, D>::MT][2],
                                              float scale_log2, WarpState<FP8, D> &st,
-                                             int lane) {
+                                             int lane, float *lg, int lg_heads) {
   float sc[4];
   block_scores<FP8, D>(sk, qf, sc, lane);
   if (nv == 16)
-    block_update<FP8, D, true>(sv, nv, sc, scale_log2, st, lane);
+    block_update<FP8, D, true, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, lg_heads);
   else
-    block_update<FP8, D, false>(sv, nv, sc, scale_log2, st, lane);
+    block_update<FP8, D, false, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, lg_heads);
 }
 
 // fp8 caches: two 16-token blocks per online-softmax step.  Their scores
 // come from independent mma chains, one shuffle reduction and one rescale
 // serve both, and both P.V products accumulate into O.  The result is the
 // same softmax, with the running maximum advanced once per pair.
-template <int D, bool FULL>
+template <int D, bool FULL, bool WEIGHTS>
 __device__ __forceinline__ void pair_update(uint32_t sva, int nva, const float (&sa)[4],
                                             uint32_t svb, int nvb, const float (&sb)[4],
-                                            float scale_log2, WarpState<true, D> &st, int lane) {
+                                            float scale_log2, WarpState<true, D> &st, int lane,
+                                            float *lga, float *lgb, int lg_heads) {
   using C = Cfg<true, D>;
   const int g = lane >> 2, c = lane & 3;
   const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -451,6 +475,10 @@ __device__ __forceinline__ void pair_update(uint32_t sva, int nva, const float (
   const float t1 = b_lo ? sb[1] * scale_log2 : -INFINITY;
   const float t2 = b_hi ? sb[2] * scale_log2 : -INFINITY;
   const float t3 = b_hi ? sb[3] * scale_log2 : -INFINITY;
+  if constexpr (WEIGHTS) {
+    keep_scores(lga, lg_heads, g, c, s0, s1, s2, s3);
+    keep_scores(lgb, lg_heads, g, c, t0, t1, t2, t3);
+  }
   float bm0 = fmaxf(fmaxf(s0, s2), fmaxf(t0, t2)), bm1 = fmaxf(fmaxf(s1, s3), fmaxf(t1, t3));
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
@@ -516,21 +544,21 @@ __device__ __forceinline__ void pair_update(uint32_t sva, int nva, const float (
   }
 }
 
-template <int D>
+template <int D, bool WEIGHTS>
 __device__ __forceinline__ void attend_pair(uint32_t ska, int nva, uint32_t skb, int nvb,
                                             const uint32_t (&qf)[Cfg<true, D>::MT][2],
                                             float scale_log2, WarpState<true, D> &st,
-                                            int lane) {
+                                            int lane, float *lga, float *lgb, int lg_heads) {
   using C = Cfg<true, D>;
   float sa[4], sb[4];
   block_scores<true, D>(ska, qf, sa, lane);
   block_scores<true, D>(skb, qf, sb, lane);
   if (nva == 16 && nvb == 16)
-    pair_update<D, true>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb, scale_log2,
-                         st, lane);
+    pair_update<D, true, WEIGHTS>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb,
+                                  scale_log2, st, lane, lga, lgb, lg_heads);
   else
-    pair_update<D, false>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb,
-                          scale_log2, st, lane);
+    pair_update<D, false, WEIGHTS>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb,
+                                   scale_log2, st, lane, lga, lgb, lg_heads);
 }
 
 // Lane 0 issues the TMA loads of one block-head (K and V tiles) into a
@@ -650,7 +678,11 @@ __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int blk, i
 // ===========================================================================
 // Decode kernel
 // ===========================================================================
-template <bool FP8, int D, int NW = 4, int RING_KB = 64>
+// WEIGHTS: every score is also kept in p.logits, and every row's (max, sum)
+// in p.part_ml, split or not, for weights_accumulate_kernel; and a NaN score
+// makes its row NaN, as the formula does (a NaN sum is carried through, also
+// past a maximum of -inf), where the other kernels write 0.
+template <bool FP8, int D, bool WEIGHTS = false, int NW = 4, int RING_KB = 64>
 __global__ void __launch_bounds__(NW * 32)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
@@ -809,6 +841,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   }
   for (; issued < pre; ++issued) issue(issued);
 
+  // WEIGHTS: this unit's kept scores, and the piece of its block j
+  float *lg_unit = nullptr;
+  if constexpr (WEIGHTS)
+    lg_unit = p.logits + (((size_t)b * p.num_kv_heads + kvh) * p.q_groups + qg) *
+                             p.logit_tokens * p.logit_heads;
+  auto lg_at = [&](int j) -> float * {
+    if constexpr (WEIGHTS)
+      return lg_unit + (size_t)j * 16 * p.logit_heads;
+    else
+      return nullptr;
+  };
+  const int lg_heads = WEIGHTS ? p.logit_heads : 0;
+
   bool failed = false;
   int i = 0;
   const int stop_at = b == p.test_fail_seq ? min(my_n, 1) : my_n;  // test hook
@@ -824,8 +869,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int ja = blk0 + j_off + i * jstep, jb = ja + jstep;
       const int nva = stage_ok[warp][sa] ? min(16, tok1 - ja * 16) : 0;
       const int nvb = stage_ok[warp][sb] ? min(16, tok1 - jb * 16) : 0;
-      attend_pair<D>(smem_u32(ring + sa * C::STAGE_BYTES), nva,
-                     smem_u32(ring + sb * C::STAGE_BYTES), nvb, qf, p.scale_log2, st, lane);
+      attend_pair<D, WEIGHTS>(smem_u32(ring + sa * C::STAGE_BYTES), nva,
+                              smem_u32(ring + sb * C::STAGE_BYTES), nvb, qf, p.scale_log2, st,
+                              lane, lg_at(ja), lg_at(jb), lg_heads);
       __syncwarp();
       if (issued < my_n) issue(issued++);
       if (issued < my_n) issue(issued++);
@@ -840,7 +886,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int j = blk0 + j_off + i * jstep;
     const int nv = stage_ok[warp][stage] ? min(16, tok1 - j * 16) : 0;
     const uint32_t sk = smem_u32(ring + stage * C::STAGE_BYTES);
-    attend_block<FP8, D>(sk, sk + C::TILE_BYTES, nv, qf, p.scale_log2, st, lane);
+    attend_block<FP8, D, WEIGHTS>(sk, sk + C::TILE_BYTES, nv, qf, p.scale_log2, st, lane, lg_at(j),
+                                  lg_heads);
     __syncwarp();
     if (issued < my_n) issue(issued++);
   }
@@ -853,6 +900,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     for (int i = 0; i < issued; ++i)
       mbar_wait_bounded(&bars[warp][i % C::STAGES], (i / C::STAGES) & 1, p.timeout_ns);
     st.m0 = st.m1 = -INFINITY;
+    // a warp that gave up contributes nothing: none of its tokens has weight
+    if constexpr (WEIGHTS) {
+      st.l0 = st.l1 = 0.f;
+      for (int i = 0; i < my_n; ++i)
+        keep_scores(lg_at(blk0 + j_off + i * jstep), lg_heads, g, c, -INFINITY, -INFINITY,
+                    -INFINITY, -INFINITY);
+    }
   }
 
   // ---- warp-owned partition: this warp's result, staged through its ring --
@@ -881,11 +935,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int h = idx / D;
       const int d = idx - h * D;
       const float2 ml = ml_w[h];
-      const bool live = !failed && ml.x != -INFINITY && ml.y > 0.f;
+      const bool live = !failed && ((ml.x != -INFINITY && ml.y > 0.f) || (WEIGHTS && ml.y != ml.y));
       const float res = live ? o_s[h * C::OS_STRIDE + d] / ml.y * p.v_scale : 0.f;
       const size_t r = row0 + h;
       if (direct) {
         p.out[r * D + d] = __float2bfloat16_rn(res);
+        if constexpr (WEIGHTS)
+          if (d == 0) p.part_ml[r * p.max_parts] = live ? ml : make_float2(-INFINITY, 0.f);
       } else {
         const size_t slot = r * p.max_parts + slot_base + part;
         p.part_o[slot * D + d] = res;
@@ -922,22 +978,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < C::NW; ++w) M = fmaxf(M, m_s[w][h]);
+    bool any = M != -INFINITY;
+    if constexpr (WEIGHTS) {  // a warp of NaN scores alone has no maximum
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) any = any || l_s[w][h] != l_s[w][h];
+    }
     float lsum = 0.f, acc = 0.f;
-    if (M != -INFINITY) {
+    if (any) {
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) {
         const float mw = m_s[w][h];
-        if (mw == -INFINITY) continue;
+        if (mw == -INFINITY && !(WEIGHTS && l_s[w][h] != l_s[w][h])) continue;
         const float e = exp2f(mw - M);
         lsum += e * l_s[w][h];
         acc += e * reinterpret_cast<const float *>(
                        rings + w * C::STAGES * C::STAGE_BYTES)[h * C::OS_STRIDE + d];
       }
     }
-    const float res = lsum > 0.f ? acc / lsum * p.v_scale : 0.f;
+    const bool live = lsum > 0.f || (WEIGHTS && lsum != lsum);
+    const float res = live ? acc / lsum * p.v_scale : 0.f;
     const size_t r = row0 + h;
     if (nparts == 1 && slot_base == 0) {
       p.out[r * D + d] = __float2bfloat16_rn(res);
+      if constexpr (WEIGHTS)
+        if (d == 0) p.part_ml[r * p.max_parts] = make_float2(M, lsum);
     } else {
       const size_t slot = r * p.max_parts + slot_base + part;
       p.part_o[slot * D + d] = res;
@@ -947,6 +1011,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   if (wait_at_exit) grid_dependency_wait();
 }
 
+// Partition j's share of a row's sum, 2^(m_j - M) l_j; an empty partition has
+// none.  WEIGHTS: a NaN sum counts even with no maximum.
+template <bool WEIGHTS>
+__device__ __forceinline__ float part_weight(float2 v, float M) {
+  if (v.x == -INFINITY && !(WEIGHTS && v.y != v.y)) return 0.f;
+  return exp2f(v.x - M) * v.y;
+}
+
 // Log-sum-exp merge of split sequences: one warp per (sequence, query head)
 // row, lane l owning head_dim elements l, l + 32, ...  Partition j carries
 // m_j (log2 domain), l_j and its normalised output o_j; the result is
@@ -954,7 +1026,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // (m, l) pairs of up to 32 partitions are loaded at once (one per lane) and
 // reduced with shuffles; outputs accumulate partition by partition, in
 // partition order.
-template <int D>
+template <int D, bool WEIGHTS>
 __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodeParams p) {
   constexpr int KD = D / 32;
   constexpr int PRE = 4;  // partitions loaded before the row's count is known
@@ -994,7 +1066,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodePar
     float M = v.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+    const float w = part_weight<WEIGHTS>(v, M);
     float t = w;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
@@ -1023,7 +1095,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodePar
       float w = 0.f;
       if (j0 + lane < nparts) {
         const float2 v = ml[j0 + lane];
-        w = v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+        w = part_weight<WEIGHTS>(v, M);
       }
       float t = w;
 #pragma unroll
@@ -1039,7 +1111,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodePar
       }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = (WEIGHTS ? wsum != 0.f : wsum > 0.f) ? 1.f / wsum : 0.f;
   __nv_bfloat16 *orow = p.out + (size_t)row * D + lane;
 #pragma unroll
   for (int k = 0; k < KD; ++k) orow[32 * k] = __float2bfloat16_rn(acc[k] * inv);
@@ -1055,7 +1127,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodePar
 constexpr int kMergeWideThreads = 256;
 constexpr int kMergeChunk = 2048;
 
-template <int D>
+template <int D, bool WEIGHTS>
 __global__ void __launch_bounds__(kMergeWideThreads)
 paged_decode_merge_wide_kernel(const DecodeParams p) {
   constexpr int NWM = kMergeWideThreads / 32;
@@ -1100,7 +1172,7 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
     __syncthreads();  // the previous chunk's weights are consumed (and red_s read)
     for (int j = tid; j < cnt; j += kMergeWideThreads) {
       const float2 v = ml[c0 + j];
-      const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+      const float w = part_weight<WEIGHTS>(v, M);
       w_s[j] = w;
       wsum += w;
     }
@@ -1153,12 +1225,98 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
       a.z += v.z;
       a.w += v.w;
     }
-    const float inv = t > 0.f ? 1.f / t : 0.f;
+    const float inv = (WEIGHTS ? t != 0.f : t > 0.f) ? 1.f / t : 0.f;
     __nv_bfloat16 *orow = p.out + (size_t)row * D + 4 * tid;  // out is only 2-byte aligned
     orow[0] = __float2bfloat16_rn(a.x * inv);
     orow[1] = __float2bfloat16_rn(a.y * inv);
     orow[2] = __float2bfloat16_rn(a.z * inv);
     orow[3] = __float2bfloat16_rn(a.w * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Running attention weights: weights[b, kvh, t] = decay * weights[b, kvh, t]
+// + sum over the kv head's query heads h of 2^(s_ht - M_h) / l_h, from the
+// kept scores s and each row's partition statistics (m_j, l_j), M = max m_j,
+// l = sum 2^(m_j - M) l_j.  A CTA takes kAccTokens tokens of one (sequence,
+// kv head); a thread owns its tokens, so every sum has a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kAccThreads = 256;
+constexpr int kAccPerThread = 4;
+constexpr int kAccTokens = kAccThreads * kAccPerThread;
+
+__global__ void __launch_bounds__(kAccThreads) weights_accumulate_kernel(const DecodeParams p) {
+  __shared__ float2 stat[8];  // (M, 1 / l) of a sub-group's heads; (0, 0) when a row is empty
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int cap = min(p.max_blocks * 16, p.max_seq_len);
+  const int L_in = __ldg(p.seq_lens + b);
+  const int L = clamp_len(L_in, cap);
+  const int t0 = blockIdx.x * kAccTokens;
+  if (t0 >= L) return;
+  const int nparts = L <= p.part_tokens ? 1 : (L + p.part_tokens - 1) / p.part_tokens;
+  // positions written by this call start from 0, whatever the row holds
+  int fresh = L;
+  if (p.k_new != nullptr && L_in == L) {
+    int n_new = 1;
+    bool ok = true;
+    if (p.new_start_loc) {
+      const int r0 = __ldg(p.new_start_loc + b), r1 = __ldg(p.new_start_loc + b + 1);
+      n_new = r1 - r0;
+      ok = n_new >= 0 && n_new <= L && r0 >= 0 && r1 <= p.num_new;
+    }
+    if (ok) fresh = L - n_new;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int HP = p.logit_heads;
+  float acc[kAccPerThread];
+#pragma unroll
+  for (int k = 0; k < kAccPerThread; ++k) acc[k] = 0.f;
+  for (int qg = 0; qg < p.q_groups; ++qg) {
+    const int heads = min(8, p.group - qg * 8);
+    if (warp < heads) {
+      const size_t row = (size_t)b * p.num_heads + (size_t)kvh * p.group + qg * 8 + warp;
+      const float2 *ml = p.part_ml + row * p.max_parts;
+      float M = -INFINITY, l = 0.f;
+      for (int j = lane; j < nparts; j += 32) M = fmaxf(M, ml[j].x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      for (int j = lane; j < nparts; j += 32) {
+        const float2 v = ml[j];
+        l += part_weight<true>(v, M);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      if (lane == 0) stat[warp] = l != 0.f ? make_float2(M, 1.f / l) : make_float2(0.f, 0.f);
+    }
+    __syncthreads();
+    const float *lg = p.logits + (((size_t)b * p.num_kv_heads + kvh) * p.q_groups + qg) *
+                                     p.logit_tokens * HP;
+#pragma unroll
+    for (int k = 0; k < kAccPerThread; ++k) {
+      const int t = t0 + k * kAccThreads + threadIdx.x;
+      if (t >= L) continue;
+      const float2 *row = reinterpret_cast<const float2 *>(lg + (size_t)t * HP);
+      for (int h = 0; h < heads; h += 2) {
+        const float2 s = __ldcs(row + h / 2);
+        const float2 a = stat[h];
+        if (a.y != 0.f) acc[k] += exp2f(s.x - a.x) * a.y;
+        if (h + 1 < heads) {
+          const float2 c = stat[h + 1];
+          if (c.y != 0.f) acc[k] += exp2f(s.y - c.x) * c.y;
+        }
+      }
+    }
+    __syncthreads();  // stat is reused by the next sub-group
+  }
+  float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
+#pragma unroll
+  for (int k = 0; k < kAccPerThread; ++k) {
+    const int t = t0 + k * kAccThreads + threadIdx.x;
+    if (t >= L) continue;
+    const float old = (p.decay != 0.f && t < fresh) ? p.decay * w[t] : 0.f;
+    w[t] = old + acc[k];
   }
 }
 
@@ -1306,7 +1464,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-template <bool FP8, int D, int NW = 4, int RING_KB = 64>
+template <bool FP8, int D, bool WEIGHTS = false, int NW = 4, int RING_KB = 64>
 pkv_status launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const DecodeParams &p,
                          cudaStream_t s) {
   using C = Cfg<FP8, D, NW, RING_KB>;
@@ -1317,7 +1475,7 @@ pkv_status launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const Dec
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
-      if (cudaFuncSetAttribute(paged_decode_kernel<FP8, D, NW, RING_KB>,
+      if (cudaFuncSetAttribute(paged_decode_kernel<FP8, D, WEIGHTS, NW, RING_KB>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::SMEM_BYTES) != cudaSuccess)
         return PKV_ERR_CUDA;
@@ -1330,20 +1488,49 @@ pkv_status launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const Dec
   // for CTA-shared partitions (Llama-8B step 95.9 vs 97.9 us part-major)
   dim3 grid = p.warp_parts ? dim3(p.num_kv_heads * p.q_groups, p.batch, grid_y)
                            : dim3(p.num_kv_heads * p.q_groups, grid_y, p.batch);
-  if (launch_pdl(paged_decode_kernel<FP8, D, NW, RING_KB>, grid, dim3(C::NW * 32), C::SMEM_BYTES, s,
+  if (launch_pdl(paged_decode_kernel<FP8, D, WEIGHTS, NW, RING_KB>, grid, dim3(C::NW * 32), C::SMEM_BYTES, s,
                  mk, mv, p) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (p.max_parts > 1) {
     const long long rows = (long long)p.batch * p.num_heads;
     const cudaError_t e =
         p.max_parts > kMergeWarpMaxParts
-            ? launch_pdl(paged_decode_merge_wide_kernel<D>, dim3((unsigned)rows),
+            ? launch_pdl(paged_decode_merge_wide_kernel<D, WEIGHTS>, dim3((unsigned)rows),
                          dim3(kMergeWideThreads), 0, s, p)
-            : launch_pdl(paged_decode_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)),
+            : launch_pdl(paged_decode_merge_kernel<D, WEIGHTS>, dim3((unsigned)((rows + 7) / 8)),
                          dim3(256), 0, s, p);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
   }
+  if constexpr (WEIGHTS) {
+    const dim3 acc((p.max_seq_len + kAccTokens - 1) / kAccTokens, p.num_kv_heads, p.batch);
+    if (acc.x > 0 && launch_pdl(weights_accumulate_kernel, acc, dim3(kAccThreads), 0, s, p) !=
+                         cudaSuccess)
+      return PKV_ERR_CUDA;
+  }
   return PKV_OK;
+}
+
+// Workspace of the decode with running weights: the split-KV partials (none
+// when no sequence can be split), every row's (max, sum) pairs, the kept
+// scores.
+struct WeightsLayout {
+  size_t ml_off, logits_off, bytes;
+  int32_t logit_tokens, logit_heads;
+};
+
+WeightsLayout weights_layout(int64_t batch, int64_t num_heads, int64_t num_kv_heads,
+                             int64_t head_dim, int64_t max_seq_len, int64_t max_parts) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int64_t group = num_heads / num_kv_heads;
+  const size_t rows = (size_t)batch * num_heads * max_parts;
+  WeightsLayout l;
+  l.logit_tokens = (int32_t)((max_seq_len + 15) / 16 * 16);
+  l.logit_heads = (int32_t)(std::min<int64_t>(8, group) + 1) & ~1;
+  l.ml_off = max_parts > 1 ? up(rows * head_dim * sizeof(float)) : 0;
+  l.logits_off = l.ml_off + up(rows * sizeof(float2));
+  l.bytes = l.logits_off + up((size_t)batch * num_kv_heads * ((group + 7) / 8) * l.logit_tokens *
+                              l.logit_heads * sizeof(float));
+  return l;
 }
 
 }  // namespace
@@ -1383,14 +1570,16 @@ extern "C" size_t paged_attention_workspace_bytes(int32_t batch, int32_t num_hea
 
 namespace {
 
-// paged_attention_decode, and with k_new / v_new the decode step (see
-// DecodeParams::k_new).
+// paged_attention_decode, with k_new / v_new the decode step (see
+// DecodeParams::k_new), and with weights the running attention weights.
 pkv_status decode_entry(const void *q, const void *k_new, const void *v_new,
                         const int32_t *new_start_loc, int64_t num_new,
                         const pkv_cache *cache, const int32_t *block_tables, int32_t max_blocks,
                         const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale,
                         void *out, int32_t max_seq_len, int32_t partition_tokens,
-                        void *workspace, size_t workspace_bytes, void *stream) {
+                        void *workspace, size_t workspace_bytes, void *stream,
+                        float *weights = nullptr, int64_t weights_stride = 0,
+                        float decay = 0.f) {
   pkv_status st = validate_cache(cache);
   if (st != PKV_OK) return st;
   if (batch < 0 || num_heads <= 0 || max_blocks <= 0 || max_seq_len < 0 ||
@@ -1422,7 +1611,21 @@ pkv_status decode_entry(const void *q, const void *k_new, const void *v_new,
   const size_t need = paged_attention_workspace_bytes(batch, num_heads, cache->num_kv_heads,
                                                       cache->head_dim, max_seq_len,
                                                       partition_tokens);
-  if (need > 0) {
+  if (weights) {
+    const WeightsLayout l = weights_layout(batch, num_heads, cache->num_kv_heads, cache->head_dim,
+                                           max_seq_len, parts64);
+    if (!workspace || workspace_bytes < l.bytes) return PKV_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.ml_off);
+    p.logits = reinterpret_cast<float *>(ws + l.logits_off);
+    p.logit_tokens = l.logit_tokens;
+    p.logit_heads = l.logit_heads;
+    p.weights = weights;
+    p.weights_stride = weights_stride;
+    p.decay = decay;
+  } else if (need > 0) {
     if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;
     const PartLayout l =
@@ -1461,11 +1664,27 @@ pkv_status decode_entry(const void *q, const void *k_new, const void *v_new,
   }
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (weights) {
+    if (fp8)
+      return cache->head_dim == 128 ? launch_decode<true, 128, true>(mk, mv, p, s)
+                                    : launch_decode<true, 64, true>(mk, mv, p, s);
+    return cache->head_dim == 128 ? launch_decode<false, 128, true>(mk, mv, p, s)
+                                  : launch_decode<false, 64, true>(mk, mv, p, s);
+  }
   if (fp8)
     return cache->head_dim == 128 ? launch_decode<true, 128>(mk, mv, p, s)
                                   : launch_decode<true, 64>(mk, mv, p, s);
   return cache->head_dim == 128 ? launch_decode<false, 128>(mk, mv, p, s)
                                 : launch_decode<false, 64>(mk, mv, p, s);
+}
+
+// Whether the new tokens' arguments of a decode step are usable.
+bool new_tokens_ok(const void *k_new, const void *v_new, const int32_t *new_start_loc,
+                   int64_t num_new_tokens, int32_t batch) {
+  if (num_new_tokens < 0 || (!new_start_loc && num_new_tokens != batch)) return false;
+  if (batch <= 0 || num_new_tokens == 0) return true;
+  return k_new && v_new &&
+         !((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15);
 }
 
 }  // namespace
@@ -1488,15 +1707,46 @@ extern "C" pkv_status paged_attention_decode_step(
     int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale,
     void *out, int32_t max_seq_len, int32_t partition_tokens, void *workspace,
     size_t workspace_bytes, void *stream) {
-  if (num_new_tokens < 0 || (!new_start_loc && num_new_tokens != batch))
-    return PKV_ERR_ARG;
+  if (!new_tokens_ok(k_new, v_new, new_start_loc, num_new_tokens, batch)) return PKV_ERR_ARG;
   const bool any = batch > 0 && num_new_tokens > 0;
-  if (any && (!k_new || !v_new ||
-              ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15)))
-    return PKV_ERR_ARG;
   return decode_entry(q, any ? k_new : nullptr, v_new, new_start_loc, num_new_tokens, cache,
                       block_tables, max_blocks, seq_lens, batch, num_heads, scale, out,
                       max_seq_len, partition_tokens, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Decode attention with running attention weights
+// ---------------------------------------------------------------------------
+extern "C" size_t paged_attention_decode_weights_workspace_bytes(
+    int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+    int32_t partition_tokens) {
+  const int32_t pt = paged_attention_partition_tokens(batch, num_heads, num_kv_heads, max_seq_len,
+                                                      partition_tokens);
+  if (pt <= 0 || batch <= 0 || head_dim <= 0) return 0;
+  const int64_t parts = std::max<int64_t>(1, ((int64_t)max_seq_len + pt - 1) / pt);
+  return weights_layout(batch, num_heads, num_kv_heads, head_dim, max_seq_len, parts).bytes;
+}
+
+extern "C" pkv_status paged_attention_decode_weights(
+    const void *q, const void *k_new, const void *v_new, const int32_t *new_start_loc,
+    int64_t num_new_tokens, const pkv_cache *cache, const int32_t *block_tables,
+    int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale,
+    void *out, float *weights, int64_t weights_stride, float decay, int32_t max_seq_len,
+    int32_t partition_tokens, void *workspace, size_t workspace_bytes, void *stream) {
+  const bool append = k_new || v_new || new_start_loc || num_new_tokens;
+  if (append && !new_tokens_ok(k_new, v_new, new_start_loc, num_new_tokens, batch))
+    return PKV_ERR_ARG;
+  if (batch > 0 && (!weights || weights_stride < max_seq_len ||
+                    (reinterpret_cast<uintptr_t>(weights) & 3)))
+    return PKV_ERR_ARG;
+  if (!std::isfinite(decay) || max_seq_len > INT32_MAX - kAccTokens) return PKV_ERR_ARG;
+  // grid limit of the accumulation (kv heads along y)
+  if (cache && cache->num_kv_heads > 65535) return PKV_ERR_ARG;
+  const bool any = batch > 0 && num_new_tokens > 0;
+  return decode_entry(q, any ? k_new : nullptr, v_new, new_start_loc, num_new_tokens, cache,
+                      block_tables, max_blocks, seq_lens, batch, num_heads, scale, out,
+                      max_seq_len, partition_tokens, workspace, workspace_bytes, stream, weights,
+                      weights_stride, decay);
 }
 
 // ---------------------------------------------------------------------------

@@ -2,8 +2,8 @@
 // 3 mantissa bits, bias 7, no infinities, NaN = S.1111.111), the cache
 // encoding of an fp8 paged KV cache: q = E4M3(RN-even, saturating to
 // +-448)(x / scale) with x / scale the IEEE binary32 quotient.  Shared by
-// the slot-mapped write and the decode step's in-kernel write of the new
-// token, so that both store the same bytes.
+// the slot-mapped write, its rotary form and the decode step's in-kernel
+// write of the new token, so that all store the same bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t quant2_e4m3(float a, float b, float scale, E
   if (r.ok && lo == hi) return lo;
   return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)),
                                   __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight binary32 values to eight E4M3 bytes.
+__device__ __forceinline__ uint2 quant8_e4m3(const float (&x)[8], float scale, E4m3Recip r) {
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = quant2_e4m3(x[2 * i], x[2 * i + 1], scale, r);
+  return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
 // Eight bf16 values to eight E4M3 bytes.

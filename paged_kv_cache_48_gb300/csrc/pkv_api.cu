@@ -43,9 +43,10 @@ using namespace pkv;
 extern "C" pkv_status pkv_check(void *stream, int64_t *detail) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (detail) *detail = -1;
-  constexpr int kUnits = 5;
+  constexpr int kUnits = 7;
   const void *sym[kUnits] = {error_word_write_zero(), error_word_attention(),
-                             error_word_blocks(), error_word_prep(), error_word_prefill()};
+                             error_word_blocks(), error_word_prep(), error_word_prefill(),
+                             error_word_rope(), error_word_evict()};
   // one 16-byte record per unit: {code, global-timer stamp}
   unsigned long long rec[kUnits][2] = {};
   for (int i = 0; i < kUnits; ++i)
@@ -84,4 +85,4 @@ extern "C" const char *pkv_status_str(pkv_status status) {
   return "unknown status";
 }
 
-extern "C" int32_t pkv_version(void) { return 200; }
+extern "C" int32_t pkv_version(void) { return 300; }

@@ -26,6 +26,8 @@ const void *error_word_attention();
 const void *error_word_blocks();
 const void *error_word_prep();
 const void *error_word_prefill();
+const void *error_word_rope();
+const void *error_word_evict();
 
 // Shared-prefix pass of cascade decode (attention_prefill.cu): for every
 // group, the members' queries against the group's prefix on the tensor

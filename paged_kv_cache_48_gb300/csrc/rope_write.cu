@@ -1,0 +1,338 @@
+// rope_write.cu -- rotary positions on several axes, fused with the
+// slot-mapped write: the step between a layer's q/k/v projection and its
+// attention.
+//
+// A token has one position on each of 1 to 4 axes (one for text; time,
+// height and width for images and video).  Pair i of a head, i < R / 2, is
+// turned by the angle a_i = position[axis[i]] * frequency[i]:
+//   (x, y) -> (x cos a - y sin a, x sin a + y cos a),
+// where the pair is elements (i, i + R / 2), or (2 i, 2 i + 1); elements from
+// R on are left alone.  q is turned into q_out; k is turned and written,
+// with v, to the token's slot of the paged cache (the slot-mapped write of
+// the vLLM concept page, compassingai.com, "15 分钟专家深入" item 2), so
+// position and slot are separate inputs: a token keeps its position when
+// other tokens are evicted and the slots move up.
+//
+// Angles are exact modulo one turn whatever the position: the host turns a
+// frequency into round(2^64 frequency / 2 pi) mod 2^64, the kernel multiplies
+// it with the position in 64-bit integers, where overflow drops exactly the
+// whole turns, and the top 32 bits are the fraction of a turn, which binary32
+// holds to 2^-26 turns.  sincospif takes it from there.  The
+// rotation is in binary32 and each result is rounded once, to bf16 or, for
+// an E4M3 cache, straight to E4M3.
+#include <algorithm>
+#include <cmath>
+#include <utility>
+
+#include "e4m3_encode.cuh"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+
+namespace pkv {
+
+static __device__ ErrorWord g_err_rope = {0ull, 0ull};
+
+constexpr int kRopeThreads = 128;
+
+struct RopeTable {  // travels in the launch parameters
+  uint64_t turns[PKV_ROPE_MAX_PAIRS];  // turns per position, times 2^64
+  uint8_t axis[PKV_ROPE_MAX_PAIRS];
+};
+
+struct RopeParams {
+  const uint4 *q, *k, *v;  // 8-element vectors
+  uint4 *q_out;
+  long long q_stride, k_stride, v_stride, out_stride;  // of a token, in vectors
+  const int32_t *positions;  // [num_axes, axis_stride]
+  long long axis_stride;
+  const int64_t *slots;
+  uint8_t *k_cache, *v_cache;
+  long long num_tokens, num_slots;
+  int num_heads, num_kv_heads, num_axes, rotary_dim;
+  int splits;  // warps that share a token's heads
+  float k_scale, v_scale;
+};
+
+// One warp takes a token's heads (or every splits-th group of them): q, k
+// and v heads in that order, 512 / D of them side by side.  A lane owns two
+// 8-element vectors of a head, the same two in every head, and with them the
+// 8 pairs they hold, so it computes the sine and cosine of a token's 8
+// angles once and uses them for all its heads; nothing is shared between
+// lanes.
+template <bool FP8, int D, bool ADJACENT>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_write_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
+  constexpr int LANES = D / 16;        // lanes of a head
+  constexpr int HEADS = 32 / LANES;    // heads side by side
+  constexpr int BATCH = 3;             // head groups whose loads go out together
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LANES, u = lane % LANES;
+  const bool turned = u < p.rotary_dim / 16;
+  // the lane's two vectors of a head
+  const int v0 = (turned && !ADJACENT) ? u : 2 * u;
+  const int v1 = (turned && !ADJACENT) ? u + p.rotary_dim / 16 : 2 * u + 1;
+
+  uint64_t turns[8];
+  int axis[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    turns[i] = turned ? table.turns[8 * u + i] : 0ull;
+    axis[i] = turned ? table.axis[8 * u + i] : 0;
+  }
+  const E4m3Recip kr = e4m3_recip(p.k_scale), vr = e4m3_recip(p.v_scale);
+  const int q_end = p.num_heads, k_end = q_end + p.num_kv_heads, all = k_end + p.num_kv_heads;
+  const int groups = (all + HEADS - 1) / HEADS;
+  const int row_vecs = p.num_kv_heads * (D / 8);
+
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
+  const long long items = p.num_tokens * p.splits;
+  for (long long item = blockIdx.x * (long long)(kRopeThreads / 32) + (threadIdx.x >> 5);
+       item < items; item += warps) {
+    const long long tok = item / p.splits;
+    const int first = (int)(item - tok * p.splits);
+    const int32_t my_pos =
+        lane < p.num_axes ? __ldg(p.positions + lane * p.axis_stride + tok) : 0;
+    const int64_t slot = __ldg(p.slots + tok);
+    const bool put = slot >= 0 && slot < p.num_slots;
+    if (slot >= p.num_slots && first == 0 && lane == 0)
+      record_error(&g_err_rope, PKV_ERR_RANGE, tok);
+
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t pos = __shfl_sync(0xffffffffu, my_pos, axis[i]);
+      const uint64_t f = turns[i] * (uint64_t)pos + 0x80000000ull;
+      sincospif((float)(int32_t)(uint32_t)(f >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+    }
+
+    for (int g0 = first; g0 < groups; g0 += BATCH * p.splits) {
+      uint4 a[BATCH], b[BATCH];
+#pragma unroll
+      for (int n = 0; n < BATCH; ++n) {
+        const int h = (g0 + n * p.splits) * HEADS + sub;
+        if (h >= all || (h >= q_end && !put)) continue;
+        const uint4 *src = h < q_end   ? p.q + tok * p.q_stride + h * (D / 8)
+                           : h < k_end ? p.k + tok * p.k_stride + (h - q_end) * (D / 8)
+                                       : p.v + tok * p.v_stride + (h - k_end) * (D / 8);
+        a[n] = src[v0];
+        b[n] = src[v1];
+      }
+#pragma unroll
+      for (int n = 0; n < BATCH; ++n) {
+        const int h = (g0 + n * p.splits) * HEADS + sub;
+        if (h >= all || (h >= q_end && !put)) continue;
+        float x[8], y[8];  // the vectors' elements
+        const uint32_t wa[4] = {a[n].x, a[n].y, a[n].z, a[n].w};
+        const uint32_t wb[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(wa[i] << 16);
+          x[2 * i + 1] = __uint_as_float(wa[i] & 0xffff0000u);
+          y[2 * i] = __uint_as_float(wb[i] << 16);
+          y[2 * i + 1] = __uint_as_float(wb[i] & 0xffff0000u);
+        }
+        if (turned && h < k_end) {
+          if (ADJACENT) {  // vector a: pairs 0..3, vector b: pairs 4..7
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float s = x[2 * i], t = x[2 * i + 1];
+              x[2 * i] = s * cs[i] - t * sn[i];
+              x[2 * i + 1] = s * sn[i] + t * cs[i];
+              s = y[2 * i], t = y[2 * i + 1];
+              y[2 * i] = s * cs[4 + i] - t * sn[4 + i];
+              y[2 * i + 1] = s * sn[4 + i] + t * cs[4 + i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float s = x[i], t = y[i];
+              x[i] = s * cs[i] - t * sn[i];
+              y[i] = s * sn[i] + t * cs[i];
+            }
+          }
+        }
+        if (FP8 && h >= q_end) {
+          const bool is_k = h < k_end;
+          const float scale = is_k ? p.k_scale : p.v_scale;
+          const E4m3Recip r = is_k ? kr : vr;
+          uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) + slot * row_vecs +
+                       (h - (is_k ? q_end : k_end)) * (D / 8);
+          dst[v0] = quant8_e4m3(x, scale, r);
+          dst[v1] = quant8_e4m3(y, scale, r);
+        } else {
+          uint4 *dst = h < q_end ? p.q_out + tok * p.out_stride + h * (D / 8)
+                       : h < k_end
+                           ? reinterpret_cast<uint4 *>(p.k_cache) + slot * row_vecs +
+                                 (h - q_end) * (D / 8)
+                           : reinterpret_cast<uint4 *>(p.v_cache) + slot * row_vecs +
+                                 (h - k_end) * (D / 8);
+          if (turned && h < k_end) {
+            a[n] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            b[n] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                              pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+          }
+          dst[v0] = a[n];  // not turned: the bits unchanged
+          dst[v1] = b[n];
+        }
+      }
+    }
+  }
+}
+
+namespace {
+
+// Whether n token rows of `a_len` bytes at a, `a_stride` bytes apart, and n
+// rows at b have no byte in common.  Rows of different strides whose spans
+// overlap count as overlapping.
+bool rows_disjoint(const void *a, int64_t a_stride, int64_t a_len, const void *b, int64_t b_stride,
+                   int64_t b_len, int64_t n) {
+  const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a);
+  const int64_t y = (int64_t)reinterpret_cast<uintptr_t>(b);
+  if (x + (n - 1) * a_stride + a_len <= y || y + (n - 1) * b_stride + b_len <= x) return true;
+  if (a_stride != b_stride || n == 1) return false;
+  const int64_t off = ((y - x) % a_stride + a_stride) % a_stride;  // of b's rows within a's stride
+  return off >= a_len && off + b_len <= a_stride;
+}
+
+// round(2^64 f / 2 pi) mod 2^64.  f / 2 pi is the sum of a double and its
+// error term (1 / 2 pi itself as a double and the rest of it); the double's
+// fraction is cut into 32 bits twice, exactly, and the error term, below
+// 2^-44, is added in units of 2^-64.
+uint64_t turns_2_64(double f) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  double turns = f * kHi;
+  const double rest = std::fma(f, kHi, -turns) + f * kLo;
+  turns -= std::floor(turns);  // may round to 1, which wraps to 0 below
+  const double scaled = turns * 4294967296.0, hi = std::floor(scaled);
+  const double lo = (scaled - hi) * 4294967296.0;
+  return ((uint64_t)hi << 32) + (uint64_t)lo + (uint64_t)std::llround(rest * 0x1p64);
+}
+
+template <bool FP8, int D>
+cudaError_t launch_rope(bool adjacent, int grid, cudaStream_t s, const RopeTable &t,
+                        const RopeParams &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return adjacent ? cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, true>, t, p)
+                  : cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, false>, t, p);
+}
+
+}  // namespace
+
+const void *error_word_rope() { return &g_err_rope; }
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const void *k,
+                                          int64_t k_stride, const void *v, int64_t v_stride,
+                                          const int32_t *positions, int64_t axis_stride,
+                                          const int64_t *slot_mapping, int64_t num_tokens,
+                                          int32_t num_heads, const pkv_rope *rope,
+                                          const pkv_cache *cache, void *q_out,
+                                          int64_t q_out_stride, void *stream) {
+  pkv_status st = validate_cache(cache);
+  if (st != PKV_OK) return st;
+  if (!rope || !rope->frequencies || !rope->axis) return PKV_ERR_ARG;
+  const int R = rope->rotary_dim, D = cache->head_dim;
+  if (R < 16 || R > D || R % 16) return PKV_ERR_SHAPE;
+  if (rope->num_axes < 1 || rope->num_axes > PKV_ROPE_MAX_AXES) return PKV_ERR_SHAPE;
+  RopeTable t = {};
+  for (int i = 0; i < R / 2; ++i) {
+    const double f = rope->frequencies[i];
+    if (!std::isfinite(f) || std::fabs(f) > 1024.0 || rope->axis[i] >= rope->num_axes)
+      return PKV_ERR_ARG;
+    t.turns[i] = turns_2_64(f);
+    t.axis[i] = rope->axis[i];
+  }
+  if (num_tokens < 0 || num_heads < 0) return PKV_ERR_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !positions || !slot_mapping || (num_heads > 0 && (!q || !q_out)))
+    return PKV_ERR_ARG;
+  const int64_t q_len = (int64_t)num_heads * D, kv_len = (int64_t)cache->num_kv_heads * D;
+  // bounds under which no byte offset below overflows
+  constexpr int64_t kMaxStride = INT64_C(1) << 30;
+  if (num_heads > INT32_MAX / 4 || cache->num_kv_heads > INT32_MAX / 8 || num_tokens > INT32_MAX ||
+      k_stride > kMaxStride || v_stride > kMaxStride ||
+      (num_heads > 0 && (q_stride > kMaxStride || q_out_stride > kMaxStride)))
+    return PKV_ERR_ARG;
+  if (k_stride < kv_len || v_stride < kv_len || axis_stride < num_tokens ||
+      (num_heads > 0 && (q_stride < q_len || q_out_stride < q_len)))
+    return PKV_ERR_ARG;
+  if ((k_stride | v_stride | (num_heads > 0 ? q_stride | q_out_stride : 0)) & 7)
+    return PKV_ERR_ARG;
+  const uintptr_t qs = num_heads > 0
+                           ? reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out)
+                           : 0;
+  if ((qs | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return PKV_ERR_ARG;
+  // q may be turned in place (a thread reads its elements before it writes
+  // them); otherwise q_out must not touch the inputs
+  if (num_heads > 0) {
+    const bool in_place = q == q_out && (q_stride == q_out_stride || num_tokens == 1);
+    if ((!in_place && !rows_disjoint(q, 2 * q_stride, 2 * q_len, q_out, 2 * q_out_stride,
+                                     2 * q_len, num_tokens)) ||
+        !rows_disjoint(k, 2 * k_stride, 2 * kv_len, q_out, 2 * q_out_stride, 2 * q_len,
+                       num_tokens) ||
+        !rows_disjoint(v, 2 * v_stride, 2 * kv_len, q_out, 2 * q_out_stride, 2 * q_len,
+                       num_tokens))
+      return PKV_ERR_ARG;
+  }
+  const bool fp8 = cache->dtype == PKV_FP8_E4M3;
+  if (fp8 && !(cache->k_scale > 0.f && cache->v_scale > 0.f)) return PKV_ERR_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PKV_ERR_CUDA;
+
+  RopeParams p = {};
+  p.q = static_cast<const uint4 *>(q);
+  p.k = static_cast<const uint4 *>(k);
+  p.v = static_cast<const uint4 *>(v);
+  p.q_out = static_cast<uint4 *>(q_out);
+  p.q_stride = q_stride / 8;
+  p.k_stride = k_stride / 8;
+  p.v_stride = v_stride / 8;
+  p.out_stride = q_out_stride / 8;
+  p.positions = positions;
+  p.axis_stride = axis_stride;
+  p.slots = slot_mapping;
+  p.k_cache = static_cast<uint8_t *>(cache->key_cache);
+  p.v_cache = static_cast<uint8_t *>(cache->value_cache);
+  p.num_tokens = num_tokens;
+  p.num_slots = (int64_t)cache->num_blocks * cache->block_size;
+  p.num_heads = num_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.num_axes = rope->num_axes;
+  p.rotary_dim = R;
+  p.k_scale = fp8 ? cache->k_scale : 1.f;
+  p.v_scale = fp8 ? cache->v_scale : 1.f;
+  // Few tokens: a token's head groups go to several warps, up to one each.
+  const int64_t heads = num_heads + 2 * (int64_t)cache->num_kv_heads;
+  const int64_t groups = (heads + 512 / D - 1) / (512 / D);
+  const int64_t target = (int64_t)sms * 32;
+  p.splits = (int)std::min<int64_t>(groups, std::max<int64_t>(1, target / num_tokens));
+  const int64_t warps = num_tokens * p.splits;
+  const int64_t want = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  const int grid = (int)std::min<int64_t>(want, (int64_t)sms * 16);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool adj = rope->interleaved != 0;
+  cudaError_t e;
+  if (fp8)
+    e = D == 128 ? launch_rope<true, 128>(adj, grid, s, t, p)
+                 : launch_rope<true, 64>(adj, grid, s, t, p);
+  else
+    e = D == 128 ? launch_rope<false, 128>(adj, grid, s, t, p)
+                 : launch_rope<false, 64>(adj, grid, s, t, p);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

@@ -15,7 +15,7 @@ import numpy as np
 import torch
 
 from . import _native
-from ._native import PagedKVError, PkvCache
+from ._native import PagedKVError, PkvCache, PkvRope
 
 BLOCK_SIZE = 16
 _DTYPES = {"bf16": _native.PKV_BF16, "fp8_e4m3": _native.PKV_FP8_E4M3}
@@ -488,6 +488,299 @@ def paged_attention_prefill(q: torch.Tensor, cache: PagedKVCache,
         _stream_handle(stream, dev))
     _native.check("paged_attention_prefill", st)
     return out
+
+
+class RotaryAxes:
+    """A rotary embedding whose positions lie on several axes (one for text;
+    time, height and width for images and video).
+
+    rotary_dim leading elements of each head turn, in rotary_dim / 2 pairs;
+    sections[a] pairs follow axis a: the first sections[0] pairs axis 0, the
+    next sections[1] axis 1, and so on, or with interleave_axes dealt in
+    turn (pair i follows axis i % A while that axis has pairs left, axis 0
+    takes the others).  Pair i is elements (i, i + rotary_dim / 2), or with
+    interleave_pairs (2 i, 2 i + 1).  Its frequency is
+    base ** (-2 i / rotary_dim) radians per position, or frequencies[i]."""
+
+    def __init__(self, rotary_dim: int, sections, base: float = 10000.0,
+                 interleave_axes: bool = False, interleave_pairs: bool = False,
+                 frequencies=None):
+        rotary_dim, sections = int(rotary_dim), [int(s) for s in sections]
+        if rotary_dim < 16 or rotary_dim > 128 or rotary_dim % 16:
+            raise ValueError("rotary_dim must be a multiple of 16, 16 .. 128")
+        pairs, A = rotary_dim // 2, len(sections)
+        if not 1 <= A <= 4:
+            raise ValueError("sections must name 1 to 4 axes")
+        if min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError("sections must be counts that sum to rotary_dim / 2")
+        if interleave_axes:
+            axis = [i % A if i < A * sections[i % A] else 0 for i in range(pairs)]
+            if [axis.count(a) for a in range(A)] != sections:
+                raise ValueError("interleave_axes: these sections cannot be dealt in turn")
+        else:
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        if frequencies is None:
+            frequencies = float(base) ** (-2.0 * np.arange(pairs) / rotary_dim)
+        self.frequencies = np.ascontiguousarray(frequencies, dtype=np.float64).reshape(-1)
+        if self.frequencies.size != pairs:
+            raise ValueError("frequencies must hold rotary_dim / 2 values")
+        self.axis = np.asarray(axis, dtype=np.uint8)
+        self.rotary_dim, self.num_axes = rotary_dim, A
+        self.interleave_pairs = bool(interleave_pairs)
+        self._struct = PkvRope(self.frequencies.ctypes.data, self.axis.ctypes.data, A,
+                               rotary_dim, int(self.interleave_pairs))
+
+    def c_struct(self) -> PkvRope:
+        return self._struct
+
+
+def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], used, call):
+    """Run call(stream handle) with `dev` current.  `used` are tensors this
+    module allocated for the call: on a stream other than torch's current
+    one, the allocator is told that they are in use there."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be on {dev}, got {stream.device}")
+        if used and stream != torch.cuda.current_stream(dev):
+            for t in used:
+                t.record_stream(stream)
+    handle = _stream_handle(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        return call(handle)
+    with torch.cuda.device(dev):
+        return call(handle)
+
+
+def _head_rows(t: torch.Tensor, name: str, dev, heads: int, dim: int) -> int:
+    """Token stride (elements) of [T, heads, dim] bf16 rows whose heads are
+    contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
+    if (t.stride(2) != 1 and dim > 1) or (t.stride(1) != dim and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
+                        v: torch.Tensor, positions: torch.Tensor,
+                        slot_mapping: torch.Tensor, cache: PagedKVCache,
+                        rope: RotaryAxes, q_out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None
+                        ) -> Optional[torch.Tensor]:
+    """Turn q and k by their tokens' positions (int32 [A, T], or [T] with one
+    axis) and write k and v into their slots (int64 [T], negative = skip).
+    q [T, Hq, d], k and v [T, num_kv_heads, d] bf16 may be slices of one
+    projection's output (a token's heads contiguous).  Returns q_out (q
+    itself turns q in place; None with q None)."""
+    dev = cache.device
+    Hkv, d = cache.num_kv_heads, cache.head_dim
+    ks = _head_rows(k, "k", dev, Hkv, d)
+    vs = _head_rows(v, "v", dev, Hkv, d)
+    T = k.shape[0]
+    _require(slot_mapping, "slot_mapping", torch.int64, dev, 1)
+    if not isinstance(rope, RotaryAxes):
+        raise TypeError("rope must be a RotaryAxes")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+        raise TypeError(f"positions must be a tensor of {torch.int32}")
+    if positions.device != dev:
+        raise ValueError(f"positions must be on {dev}, got {positions.device}")
+    if positions.dim() == 1:
+        positions = positions[None]
+    if tuple(positions.shape) != (rope.num_axes, T) or (T > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions must be [{rope.num_axes}, {T}] with contiguous rows")
+    if v.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("k, v, slot_mapping must name the same tokens")
+    used = []
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        Hq, q_args, out_args = 0, (None, 0), (None, 0)
+    else:
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+        qs = _head_rows(q, "q", dev, Hq, d)
+        if q.shape[0] != T:
+            raise ValueError("q and k must name the same tokens")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            used.append(q_out)
+        os = _head_rows(q_out, "q_out", dev, Hq, d)
+        if q_out.shape[0] != T:
+            raise ValueError("q_out must have q's shape")
+        q_args, out_args = (q.data_ptr(), qs), (q_out.data_ptr(), os)
+    axis_stride = positions.stride(0) if rope.num_axes > 1 else T
+    st = _launch(dev, stream, used, lambda s: _native.lib().paged_kv_rope_write(
+        *q_args, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+        axis_stride, slot_mapping.data_ptr(), T, Hq,
+        ctypes.byref(rope.c_struct()), ctypes.byref(cache.c_struct()),
+        *out_args, s))
+    _native.check("paged_kv_rope_write", st)
+    return q_out
+
+
+def paged_attention_decode_weights_workspace_bytes(
+        batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
+        max_seq_len: int, partition_tokens: int = 0) -> int:
+    """Device workspace bytes paged_attention_decode_weights needs."""
+    return int(_native.lib().paged_attention_decode_weights_workspace_bytes(
+        batch, num_heads, num_kv_heads, head_dim, max_seq_len,
+        partition_tokens))
+
+
+def paged_attention_decode_weights(q: torch.Tensor, cache: PagedKVCache,
+                                   block_tables: torch.Tensor,
+                                   seq_lens: torch.Tensor, scale: float,
+                                   max_seq_len: int, weights: torch.Tensor,
+                                   decay: float = 1.0,
+                                   k_new: Optional[torch.Tensor] = None,
+                                   v_new: Optional[torch.Tensor] = None,
+                                   new_start_loc: Optional[torch.Tensor] = None,
+                                   out: Optional[torch.Tensor] = None,
+                                   partition_tokens: int = 0,
+                                   workspace: Optional[torch.Tensor] = None,
+                                   stream: Optional[torch.cuda.Stream] = None
+                                   ) -> torch.Tensor:
+    """paged_attention_decode (with k_new and v_new
+    paged_attention_decode_step) that also updates weights, fp32 [B,
+    num_kv_heads, S >= max_seq_len]: every cached token's running attention
+    weight becomes decay times itself plus its weight in this step, summed
+    over the kv head's query heads; positions written by the call start
+    from 0.  Returns out [B, Hq, d] bf16."""
+    dev = cache.device
+    _require(q, "q", torch.bfloat16, dev, 3)
+    _require(block_tables, "block_tables", torch.int32, dev, 2)
+    _require(seq_lens, "seq_lens", torch.int32, dev, 1)
+    _require(weights, "weights", torch.float32, dev, 3)
+    B, Hq, d = q.shape
+    Hkv = cache.num_kv_heads
+    if d != cache.head_dim or block_tables.shape[0] != B or \
+            seq_lens.shape[0] != B:
+        raise ValueError("q, block_tables, seq_lens shapes do not match")
+    if tuple(weights.shape[:2]) != (B, Hkv) or weights.shape[2] < max_seq_len:
+        raise ValueError(f"weights must be [{B}, {Hkv}, >= {max_seq_len}]")
+    used = []
+    if out is None:
+        out = torch.empty_like(q)
+        used.append(out)
+    else:
+        _require(out, "out", torch.bfloat16, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    new = (None, None, None, 0)
+    if k_new is not None or v_new is not None or new_start_loc is not None:
+        n_new = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else -1
+        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+            _require(t, n, torch.bfloat16, dev, 3)
+            if t.shape != (n_new, Hkv, d):
+                raise ValueError(f"{n} must be [num_new, num_kv_heads, head_dim]")
+        nsl = None
+        if new_start_loc is not None:
+            _require(new_start_loc, "new_start_loc", torch.int32, dev, 1)
+            if new_start_loc.shape[0] != B + 1:
+                raise ValueError("new_start_loc must be [batch + 1]")
+            nsl = new_start_loc.data_ptr()
+        elif n_new != B:
+            raise ValueError("without new_start_loc, k_new holds one row per sequence")
+        new = (k_new.data_ptr(), v_new.data_ptr(), nsl, n_new)
+    if workspace is None:
+        workspace = torch.empty(
+            max(1, paged_attention_decode_weights_workspace_bytes(
+                B, Hq, Hkv, d, max_seq_len, partition_tokens)),
+            dtype=torch.uint8, device=dev)
+        used.append(workspace)
+    _require(workspace, "workspace", torch.uint8, dev, 1)
+    st = _launch(dev, stream, used, lambda s: _native.lib().paged_attention_decode_weights(
+        q.data_ptr(), *new, ctypes.byref(cache.c_struct()),
+        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+        B, Hq, float(scale), out.data_ptr(), weights.data_ptr(),
+        weights.shape[2], float(decay), int(max_seq_len),
+        int(partition_tokens), workspace.data_ptr(), workspace.numel(), s))
+    _native.check("paged_attention_decode_weights", st)
+    return out
+
+
+def paged_kv_evict_workspace_bytes(batch: int, num_kv_heads: int,
+                                   weights_width: int, max_keep: int) -> int:
+    """Device workspace bytes paged_kv_evict needs (weights_width: the last
+    dimension of weights)."""
+    return int(_native.lib().paged_kv_evict_workspace_bytes(
+        batch, num_kv_heads, weights_width, max_keep))
+
+
+def paged_kv_evict(cache: PagedKVCache, block_tables: torch.Tensor,
+                   seq_lens: torch.Tensor, weights: torch.Tensor,
+                   keep: torch.Tensor, max_keep: int, sink: int = 0,
+                   recent: int = 0, per_head: bool = True,
+                   dst_tables: Optional[torch.Tensor] = None,
+                   dst_weights: Optional[torch.Tensor] = None,
+                   new_seq_lens: Optional[torch.Tensor] = None,
+                   kept: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Cut each sequence to min(seq_lens[b], keep[b]) tokens: its last
+    `recent`, its first `sink` and the largest of weights (fp32 [B,
+    num_kv_heads, S]; equal weights: the lower position), each kv head for
+    itself or, with per_head False, all heads by their sum.  Kept rows move
+    to positions 0 .. n-1 in order, in place or into the blocks of
+    dst_tables, and their weights with them, in place or into dst_weights;
+    positions given up get weight 0.  keep int32 [B] is on the device,
+    max_keep bounds the lengths left.  kept (int32 [B, num_kv_heads or 1,
+    max_keep]), when given, receives the old positions, -1 past n.  Returns
+    new_seq_lens int32 [B] (which may be seq_lens, to update it)."""
+    dev = cache.device
+    max_keep = int(max_keep)
+    _require(block_tables, "block_tables", torch.int32, dev, 2)
+    _require(seq_lens, "seq_lens", torch.int32, dev, 1)
+    _require(weights, "weights", torch.float32, dev, 3)
+    _require(keep, "keep", torch.int32, dev, 1)
+    B, Hkv = seq_lens.shape[0], cache.num_kv_heads
+    if block_tables.shape[0] != B or keep.shape[0] != B or \
+            tuple(weights.shape[:2]) != (B, Hkv):
+        raise ValueError("block_tables, seq_lens, weights, keep shapes do not match")
+    dst, dst_blocks, dst_w, dst_stride, kept_ptr = None, 0, None, 0, None
+    if dst_tables is not None:
+        _require(dst_tables, "dst_tables", torch.int32, dev, 2)
+        if dst_tables.shape[0] != B or dst_tables.shape[1] < 1:
+            raise ValueError("dst_tables must have a row of blocks per sequence")
+        dst, dst_blocks = dst_tables.data_ptr(), dst_tables.shape[1]
+    if dst_weights is not None:
+        _require(dst_weights, "dst_weights", torch.float32, dev, 3)
+        if tuple(dst_weights.shape[:2]) != (B, Hkv) or dst_weights.shape[2] < 1:
+            raise ValueError(f"dst_weights must be [{B}, {Hkv}, >= 1]")
+        dst_w, dst_stride = dst_weights.data_ptr(), dst_weights.shape[2]
+    if kept is not None:
+        _require(kept, "kept", torch.int32, dev, 3)
+        shape = (B, Hkv if per_head else 1, max_keep)
+        if tuple(kept.shape) != shape:
+            raise ValueError(f"kept must have shape {shape}")
+        kept_ptr = kept.data_ptr()
+    used = []
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+        used.append(new_seq_lens)
+    _require(new_seq_lens, "new_seq_lens", torch.int32, dev, 1)
+    if new_seq_lens.shape[0] != B:
+        raise ValueError("new_seq_lens must have an entry per sequence")
+    if workspace is None:
+        workspace = torch.empty(
+            max(1, paged_kv_evict_workspace_bytes(B, Hkv, weights.shape[2], max_keep)),
+            dtype=torch.uint8, device=dev)
+        used.append(workspace)
+    _require(workspace, "workspace", torch.uint8, dev, 1)
+    st = _launch(dev, stream, used, lambda s: _native.lib().paged_kv_evict(
+        ctypes.byref(cache.c_struct()), block_tables.data_ptr(),
+        block_tables.shape[1], seq_lens.data_ptr(), weights.data_ptr(),
+        weights.shape[2], keep.data_ptr(), B, max_keep, int(sink),
+        int(recent), int(bool(per_head)), dst, dst_blocks, dst_w, dst_stride,
+        new_seq_lens.data_ptr(), kept_ptr, workspace.data_ptr(),
+        workspace.numel(), s))
+    _native.check("paged_kv_evict", st)
+    return new_seq_lens
 
 
 def pkv_check(stream: Optional[torch.cuda.Stream] = None, device=None):
