@@ -11,12 +11,13 @@
 // describe only whole sequences leaving the cache (vLLM concept page,
 // compassingai.com, preemption); keeping part of one is this library's.
 //
-// Two launches.  evict_select_kernel: one CTA per choice finds the weight
+// Two launches.  evict_select_kernel: one cluster per choice finds the weight
 // of the last kept token by radix selection over order-preserving 32-bit
 // keys, then writes the kept positions in ascending order.  The second
 // launch moves the rows: evict_gather_kernel into other blocks, every row
 // independent, or evict_compact_kernel in place.
 #include <algorithm>
+#include <mutex>
 #include <utility>
 
 #include "pkv_device.cuh"
@@ -50,27 +51,93 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The ranking weight of token t: the head's, or the heads' sum (in binary64,
-// heads in order, rounded once).
-__device__ __forceinline__ float rank_weight(const EvictParams &p, int b, int h, int t) {
-  const float *w = p.weights + (size_t)b * p.num_kv_heads * p.weights_stride;
-  if (p.choices > 1 || p.num_kv_heads == 1) return w[(size_t)h * p.weights_stride + t];
+// a + b in two binary32 terms without error (Knuth's two-term sum).
+__device__ __forceinline__ float two_sum(float a, float b, float &err) {
+  const float s = __fadd_rn(a, b);
+  const float z = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
+  return s;
+}
+
+// The ranking weight of token t: the head's, or the heads' sum, carried as
+// two binary32 terms (48 bits) and rounded once.  Binary64 additions would
+// cost 16 cycles of an SM per warp each (two lanes a cycle): they are left to
+// sums that meet an infinity or a NaN, where the error terms say nothing.
+template <bool SUM>
+__device__ __forceinline__ float rank_weight(const EvictParams &p, const float *row, int t) {
+  const float *w = row + t;
+  if (!SUM) return __ldg(w);
+  float hi = 0.f, lo = 0.f, e;
+#pragma unroll 8
+  for (int k = 0; k < p.num_kv_heads; ++k) {
+    hi = two_sum(hi, __ldg(w + (size_t)k * p.weights_stride), e);
+    lo = __fadd_rn(lo, e);
+  }
+  const float sum = __fadd_rn(hi, lo);
+  if (isfinite(sum)) return sum;
   double s = 0.0;
-  for (int k = 0; k < p.num_kv_heads; ++k) s += (double)w[(size_t)k * p.weights_stride + t];
+  for (int k = 0; k < p.num_kv_heads; ++k) s += (double)__ldg(w + (size_t)k * p.weights_stride);
   return (float)s;
 }
 
+// Thread-block clusters (sm_90 and later): rank, size, barrier, and a load
+// from another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int load_cluster(const int *local, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Selection.  A cluster of C CTAs takes one choice (a row of weights); CTA r
+// holds the r-th piece of the row's keys in shared memory, read from memory
+// once.  Four rounds of 8 bits from the top find the k-th largest key: each
+// CTA counts its keys that share the bits found so far by their next digit,
+// then every CTA adds up all the counts and finds the digit for itself.  What
+// bounds it is latency: a round is a pass over the keys in shared memory, one
+// cluster barrier and one read of the others' counts (256 digits: with 2048
+// in three rounds the CTAs moved 64 KB between them in each and a round took
+// over twice as long).
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectMaxCluster = 8;  // the portable size
+// Keys a CTA holds (more are read again in every round): three CTAs fit an
+// SM with them, and 8 CTAs hold 131072.
+constexpr int kSelectMaxKeys = 16 * 1024;
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int pick[2];  // digit, elements wanted within it
-  __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int h = blockIdx.x, b = blockIdx.y;
+// Sum over the warps before this one of per-warp values in shared memory.
+__device__ __forceinline__ int warps_before(const int *v, int warp, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < warp ? v[lane] : 0);
+}
+
+template <bool SUM>
+__global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
+    evict_select_kernel(const EvictParams p, int key_cap) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ int hist[4][256];
+  __shared__ int totals[2];  // this CTA's keys above the last kept one's, and equal
+  __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
+  __shared__ int pick[2];  // digit, keys wanted within it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster_rank(), C = cluster_size();
+  const int h = blockIdx.x / C, b = blockIdx.y;
+  for (int i = tid; i < 4 * 256; i += kSelectThreads) hist[i >> 8][i & 255] = 0;
+  grid_dependency_wait();
   int32_t *kept = p.kept + ((size_t)b * p.choices + h) * p.max_keep;
 
   const int L = __ldg(p.seq_lens + b), want = __ldg(p.keep + b);
@@ -78,104 +145,188 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   const bool bad = L < 0 || want < 0 || (long long)L > (long long)p.max_blocks * 16 ||
                    L > p.weights_stride || n > p.max_keep || n > p.dst_stride ||
                    (long long)n > (long long)p.dst_max_blocks * 16;
-  if (h == 0 && tid == 0) {
+  if (blockIdx.x == 0 && tid == 0) {
     p.counts[b] = make_int2(bad ? -1 : n, L);
     if (bad) record_error(&g_err_evict, PKV_ERR_RANGE, b);
   }
-  for (int i = (bad ? 0 : n) + tid; i < p.max_keep; i += kSelectThreads) kept[i] = -1;
-  if (bad) return;
+  if (bad) return;  // (the same in every CTA of the cluster, like the returns below)
+  const int all = rank * kSelectThreads + tid, step = C * kSelectThreads;  // within the cluster
   const int recent = min(p.recent, n), sink = min(p.sink, n - recent);
   // the middle: tokens sink .. L - recent - 1, of which k are kept
   const int mid = L - recent - sink, k = n - recent - sink;
-  for (int i = tid; i < sink; i += kSelectThreads) kept[i] = i;
-  for (int i = tid; i < recent; i += kSelectThreads) kept[n - recent + i] = L - recent + i;
-  if (!p.weights_in_place) {
-    // positions given up start from 0 (in place: once their weights are read)
-    const int end = (int)min((long long)L, p.dst_stride);
-    for (int hh = p.choices > 1 ? h : 0; hh < (p.choices > 1 ? h + 1 : p.num_kv_heads); ++hh) {
-      float *w = p.dst_weights + ((size_t)b * p.num_kv_heads + hh) * p.dst_stride;
-      for (int t = n + tid; t < end; t += kSelectThreads) w[t] = 0.f;
-    }
-  }
+  for (int i = all; i < sink; i += step) kept[i] = i;
+  for (int i = all; i < recent; i += step) kept[n - recent + i] = L - recent + i;
   if (k == 0) return;
   if (k == mid) {
-    for (int i = tid; i < mid; i += kSelectThreads) kept[sink + i] = sink + i;
+    for (int i = all; i < mid; i += step) kept[sink + i] = sink + i;
     return;
   }
 
-  // the k-th largest key, 8 bits at a time from the top
-  uint32_t prefix = 0;
-  int left = k;  // wanted among the keys that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < mid; i += kSelectThreads) {
-      const uint32_t key = weight_key(rank_weight(p, b, h, sink + i));
-      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+  // this CTA's piece of the middle, in the head's weights or (SUM) the first
+  // head's, the others' a stride apart
+  const float *row = p.weights + ((size_t)b * p.num_kv_heads + h) * p.weights_stride;
+  const int piece = ((mid + C - 1) / C + 31) & ~31;
+  const int base = sink + min(mid, rank * piece);
+  const int m = min(mid, (rank + 1) * piece) - min(mid, rank * piece);
+  const int held = min(m, key_cap);
+  constexpr int U = SUM ? 2 : 4;  // tokens of a thread whose loads go out together
+  // the key of every token of the piece once, to f(index, key)
+  auto read_keys = [&](int from, auto f) {
+    for (int i0 = from + tid; i0 < m; i0 += U * kSelectThreads) {
+      float w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kSelectThreads;
+        w[u] = i < m ? rank_weight<SUM>(p, row, base + i) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kSelectThreads;
+        if (i < m) f(i, weight_key(w[u]));
+      }
     }
+  };
+  __syncthreads();  // hist is zero
+  read_keys(0, [&](int i, uint32_t key) {
+    if (i < held) keys[i] = key;
+    atomicAdd(&hist[0][key >> 24], 1);
+  });
+
+  uint32_t prefix = 0;  // the k-th largest key's bits found so far
+  int left = k;         // wanted among the keys that share them
+#pragma unroll 1
+  for (int round = 0; round < 4; ++round) {
+    const int shift = 24 - 8 * round;
+    if (round > 0) {
+      auto count = [&](int, uint32_t key) {
+        if ((key >> (shift + 8)) == prefix) atomicAdd(&hist[round][(key >> shift) & 255], 1);
+      };
+      const int whole = held >> 2;  // four keys a load
+#pragma unroll 2
+      for (int v = tid; v < whole; v += kSelectThreads) {
+        const uint4 q = reinterpret_cast<const uint4 *>(keys)[v];
+        count(0, q.x);
+        count(0, q.y);
+        count(0, q.z);
+        count(0, q.w);
+      }
+      if (tid < (held & 3)) count(0, keys[4 * whole + tid]);
+      read_keys(held, count);
+    }
+    int c = 0;  // thread t < 256: the cluster's count of digit 255 - t
+    if (C > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    if (tid < 256) {
+      const int *own = &hist[round][255 - tid];
+      if (C > 1) {
+        int part[kSelectMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kSelectMaxCluster; ++r) part[r] = r < C ? load_cluster(own, r) : 0;
+#pragma unroll
+        for (int r = 0; r < kSelectMaxCluster; ++r) c += part[r];
+      } else {
+        c = *own;
+      }
+    }
+    int upto = c;  // keys of this warp's digits down to this thread's
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    if (lane == 31) warp_a[warp] = upto;
     __syncthreads();
-    if (warp == 0) {
-      // lane l holds digits 255 - 8 l .. 248 - 8 l: counts from the top
-      int c[8], sum = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c[j] = hist[255 - 8 * lane - j];
-        sum += c[j];
-      }
-      int above = sum;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, above, off);
-        if (lane >= off) above += o;
-      }
-      above -= sum;  // elements with a higher digit than this lane's first
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (above < left && left <= above + c[j]) {
-          pick[0] = 255 - 8 * lane - j;
-          pick[1] = left - above;
-        }
-        above += c[j];
-      }
+    const int above = warps_before(warp_a, warp, lane) + upto - c;  // keys with a larger digit
+    if (above < left && left <= above + c) {
+      pick[0] = 255 - tid;
+      pick[1] = left - above;
     }
     __syncthreads();
     prefix = (prefix << 8) | (uint32_t)pick[0];
     left = pick[1];
-    __syncthreads();
   }
-  // kept: every key above `prefix`, and the first `left` keys equal to it.
-  // A warp owns a contiguous piece of the middle: count, scan, write.
-  const int piece = (mid + kSelectThreads - 1) / kSelectThreads * 32;
-  const int p0 = min(mid, warp * piece), p1 = min(mid, p0 + piece);
+
+  // The moves may launch once every CTA is here (earlier, their waiting CTAs
+  // made the selection for eight rows of 131072 tokens 30 us slower).
+  allow_dependent_launch();
+  // Kept: every key above `prefix`, and the first `left` keys equal to it.
+  // A warp owns a contiguous part of the piece: count, scan, write; a lane
+  // takes four neighbouring keys at a time.
+  const int part = ((m + kSelectWarps - 1) / kSelectWarps + 127) & ~127;
+  const int p0 = min(m, warp * part), p1 = min(m, p0 + part);
+  // bit j of the low byte: key i + j is above, of the next byte: equal
+  auto flags = [&](int i) -> uint32_t {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (i + 3 < held) {
+      q = *reinterpret_cast<const uint4 *>(keys + i);
+    } else {
+      auto at = [&](int j) -> uint32_t {
+        return j >= p1     ? 0u
+               : j < held ? keys[j]
+                          : weight_key(rank_weight<SUM>(p, row, base + j));
+      };
+      q = make_uint4(at(i), at(i + 1), at(i + 2), at(i + 3));
+    }
+    const uint32_t in = i + 3 < p1 ? 0xfu : (1u << max(0, p1 - i)) - 1u;
+    const uint32_t gt = (q.x > prefix) | (q.y > prefix) << 1 | (q.z > prefix) << 2 |
+                        (q.w > prefix) << 3;
+    const uint32_t eq = (q.x == prefix) | (q.y == prefix) << 1 | (q.z == prefix) << 2 |
+                        (q.w == prefix) << 3;
+    return (gt & in) | (eq & in) << 8;
+  };
   int gt = 0, eq = 0;
-  for (int i0 = p0; i0 < p1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < p1 ? weight_key(rank_weight(p, b, h, sink + i)) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < p1 && key > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < p1 && key == prefix));
+#pragma unroll 2
+  for (int i = p0 + 4 * lane; i < p1; i += 128) {
+    const uint32_t f = flags(i);
+    gt += __popc(f & 0xffu);
+    eq += __popc(f >> 8);
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
-    warp_gt[warp] = gt;
-    warp_eq[warp] = eq;
+    warp_a[warp] = gt;
+    warp_b[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  for (int w = 0; w < warp; ++w) {
-    gt += warp_gt[w];
-    eq += warp_eq[w];
+  const int my_gt = gt, my_eq = eq;
+  gt = warps_before(warp_a, warp, lane);
+  eq = warps_before(warp_b, warp, lane);
+  if (C > 1) {
+    if (tid == kSelectThreads - 1) {
+      totals[0] = gt + my_gt;
+      totals[1] = eq + my_eq;
+    }
+    cluster_sync();
+    gt += __reduce_add_sync(0xffffffffu, lane < rank ? load_cluster(&totals[0], lane) : 0);
+    eq += __reduce_add_sync(0xffffffffu, lane < rank ? load_cluster(&totals[1], lane) : 0);
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = p0; i0 < p1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < p1 ? weight_key(rank_weight(p, b, h, sink + i)) : 0u;
-    const uint32_t m_gt = __ballot_sync(0xffffffffu, i < p1 && key > prefix);
-    const uint32_t m_eq = __ballot_sync(0xffffffffu, i < p1 && key == prefix);
-    const int my_eq = eq + __popc(m_eq & below);
-    if (i < p1 && (key > prefix || (key == prefix && my_eq < left)))
-      kept[sink + gt + __popc(m_gt & below) + min(my_eq, left)] = sink + i;
-    gt += __popc(m_gt);
-    eq += __popc(m_eq);
+  for (int i0 = p0; i0 < p1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint32_t f = flags(i);
+    // keys above (low half) and equal (high half) in the lanes up to this one
+    const uint32_t mine = __popc(f & 0xffu) | __popc(f >> 8) << 16;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    int g = gt + (int)((upto - mine) & 0xffffu), e = eq + (int)((upto - mine) >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool above = f >> j & 1, equal = f >> (8 + j) & 1;
+      if (above || (equal && e < left)) kept[sink + g + min(e, left)] = base + i + j;
+      g += above;
+      e += equal;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
+    gt += total & 0xffffu;
+    eq += total >> 16;
   }
+  // no CTA leaves while another may still read its shared memory
+  if (C > 1) cluster_sync();
 }
 
 // Row index (head rows of the pool) of position t through a table row; -1
@@ -188,6 +339,21 @@ __device__ __forceinline__ long long row_of(const EvictParams &p, const int32_t 
     return -1;
   }
   return ((long long)blk * 16 + (t & 15)) * p.num_kv_heads + h;
+}
+
+// What a row still needs besides its moves, by `step` threads: -1 past the
+// kept positions, and 0 for the weights of positions given up (weights moved
+// in place: once they are read, in evict_compact_kernel).
+__device__ __forceinline__ void finish_row(const EvictParams &p, int b, int h, int2 c, int first,
+                                           int step) {
+  if (h < p.choices) {
+    int32_t *kept = p.kept + ((size_t)b * p.choices + h) * p.max_keep;
+    for (int i = max(c.x, 0) + first; i < p.max_keep; i += step) kept[i] = -1;
+  }
+  if (c.x < 0 || p.weights_in_place) return;
+  float *w = p.dst_weights + ((size_t)b * p.num_kv_heads + h) * p.dst_stride;
+  const int end = (int)min((long long)c.y, p.dst_stride);
+  for (int t = c.x + first; t < end; t += step) w[t] = 0.f;
 }
 
 // Into other blocks: a warp moves 32 tokens of one (sequence, kv head).
@@ -207,8 +373,9 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
   const int n = c.x;
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.new_seq_lens[b] = n < 0 ? c.y : n;
   const int i0 = (blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5)) * 32;
-  if (i0 >= n) return;
   const int i = i0 + lane;
+  finish_row(p, b, h, c, blockIdx.x * kGatherThreads + threadIdx.x, gridDim.x * kGatherThreads);
+  if (i0 >= n) return;
   long long src = -1, dst = -1;
   if (i < n) {
     const int t =
@@ -269,7 +436,8 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Ev
   const int n = c.x, L = c.y;
   if (plane == 0 && h == 0 && tid == 0) p.new_seq_lens[b] = n < 0 ? L : n;
   const bool moves = p.dst_tables == p.tables;  // K and V in place
-  if (n < 0) return;                            // left alone
+  if (moves) finish_row(p, b, h, c, plane * kCompactThreads + tid, 3 * kCompactThreads);
+  if (n < 0) return;  // left alone
   const int32_t *kept = p.kept + ((size_t)b * p.choices + (p.choices > 1 ? h : 0)) * p.max_keep;
   if (plane == 2) {
     const size_t bh = (size_t)b * p.num_kv_heads + h;
@@ -343,6 +511,51 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The selection: a cluster per choice, of as many CTAs as hold a row's keys,
+// or more of them (at least 1024 keys each) while all fit the GPU at once.
+template <bool SUM>
+cudaError_t launch_select(const EvictParams &p, cudaStream_t s) {
+  const int64_t longest = std::min<int64_t>(p.weights_stride, (int64_t)p.max_blocks * 16);
+  const int64_t rows = (int64_t)p.choices * p.batch, slots = 3 * (int64_t)device_sm_count();
+  int C = 1;
+  while (C < kSelectMaxCluster &&
+         (longest > (int64_t)C * kSelectMaxKeys ||
+          (rows * C * 2 <= slots && longest >= (int64_t)C * 2048)))
+    C *= 2;
+  const int64_t piece = ((longest + C - 1) / C + 31) / 32 * 32;
+  const int cap = (int)std::min<int64_t>(std::max<int64_t>(piece, 32), kSelectMaxKeys);
+  static int configured[64] = {0};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!configured[dev]) {
+      e = cudaFuncSetAttribute(evict_select_kernel<SUM>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSelectMaxKeys * (int)sizeof(uint32_t));
+      if (e != cudaSuccess) return e;
+      configured[dev] = 1;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.choices * C, p.batch);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = cap * sizeof(uint32_t);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<SUM>, p, cap);
 }
 
 template <int RB>
@@ -441,8 +654,8 @@ extern "C" pkv_status paged_kv_evict(const pkv_cache *cache, const int32_t *bloc
   p.recent = recent;
   p.row_bytes = cache->head_dim * (cache->dtype == PKV_FP8_E4M3 ? 1 : 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (launch_pdl(evict_select_kernel, dim3(p.choices, batch), dim3(kSelectThreads), s, p) !=
-      cudaSuccess)
+  const bool sum = p.choices < p.num_kv_heads;  // one choice by the heads' sum
+  if ((sum ? launch_select<true>(p, s) : launch_select<false>(p, s)) != cudaSuccess)
     return PKV_ERR_CUDA;
   const cudaError_t e = p.row_bytes == 256   ? launch_move<256>(p, s)
                         : p.row_bytes == 128 ? launch_move<128>(p, s)
