@@ -534,37 +534,46 @@ class RotaryAxes:
         return self._struct
 
 
-def _launch(dev: torch.device, stream: Optional[torch.cuda.Stream], used, call):
-    """Run call(stream handle) with `dev` current.  `used` are tensors this
+def _launch(fn, args, dev: torch.device, stream: Optional[torch.cuda.Stream], used) -> int:
+    """fn(*args, stream handle) with `dev` current.  `used` are tensors this
     module allocated for the call: on a stream other than torch's current
     one, the allocator is told that they are in use there."""
-    if stream is not None:
+    if stream is None:
+        handle = _raw_stream(dev.index)
+    else:
         if stream.device != dev:
             raise ValueError(f"stream must be on {dev}, got {stream.device}")
         if used and stream != torch.cuda.current_stream(dev):
             for t in used:
                 t.record_stream(stream)
-    handle = _stream_handle(stream, dev)
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        return call(handle)
+        return fn(*args, handle)
     with torch.cuda.device(dev):
-        return call(handle)
+        return fn(*args, handle)
 
 
-def _head_rows(t: torch.Tensor, name: str, dev, heads: int, dim: int) -> int:
-    """Token stride (elements) of [T, heads, dim] bf16 rows whose heads are
-    contiguous."""
+def _raw_stream(index: int) -> int:
+    """Handle of torch's current stream on a device."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _head_rows(t: torch.Tensor, name: str, dev, heads: int, dim: int):
+    """(tokens, token stride in elements) of [T, heads, dim] bf16 rows whose
+    heads are contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
-    if (t.stride(2) != 1 and dim > 1) or (t.stride(1) != dim and heads > 1):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    token, head, element = t.stride()
+    if element != 1 or (head != dim and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return shape[0], token if shape[0] > 1 else heads * dim
 
 
 def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
@@ -578,11 +587,11 @@ def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
     q [T, Hq, d], k and v [T, num_kv_heads, d] bf16 may be slices of one
     projection's output (a token's heads contiguous).  Returns q_out (q
     itself turns q in place; None with q None)."""
-    dev = cache.device
-    Hkv, d = cache.num_kv_heads, cache.head_dim
-    ks = _head_rows(k, "k", dev, Hkv, d)
-    vs = _head_rows(v, "v", dev, Hkv, d)
-    T = k.shape[0]
+    key_cache = cache.key_cache
+    dev = key_cache.device
+    _, _, Hkv, d = key_cache.shape
+    T, ks = _head_rows(k, "k", dev, Hkv, d)
+    Tv, vs = _head_rows(v, "v", dev, Hkv, d)
     _require(slot_mapping, "slot_mapping", torch.int64, dev, 1)
     if not isinstance(rope, RotaryAxes):
         raise TypeError("rope must be a RotaryAxes")
@@ -590,35 +599,31 @@ def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
         raise TypeError(f"positions must be a tensor of {torch.int32}")
     if positions.device != dev:
         raise ValueError(f"positions must be on {dev}, got {positions.device}")
-    if positions.dim() == 1:
-        positions = positions[None]
-    if tuple(positions.shape) != (rope.num_axes, T) or (T > 1 and positions.stride(1) != 1):
-        raise ValueError(f"positions must be [{rope.num_axes}, {T}] with contiguous rows")
-    if v.shape[0] != T or slot_mapping.shape[0] != T:
+    A = rope.num_axes
+    shape, stride = positions.shape, positions.stride()
+    if not (shape == (A, T) or (A == 1 and shape == (T,))) or (T > 1 and stride[-1] != 1):
+        raise ValueError(f"positions must be [{A}, {T}] with contiguous rows")
+    if Tv != T or slot_mapping.shape[0] != T:
         raise ValueError("k, v, slot_mapping must name the same tokens")
-    used = []
+    used = ()
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
-        Hq, q_args, out_args = 0, (None, 0), (None, 0)
+        Hq, qp, qs, op, os = 0, None, 0, None, 0
     else:
         Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        qs = _head_rows(q, "q", dev, Hq, d)
-        if q.shape[0] != T:
-            raise ValueError("q and k must name the same tokens")
+        Tq, qs = _head_rows(q, "q", dev, Hq, d)
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-            used.append(q_out)
-        os = _head_rows(q_out, "q_out", dev, Hq, d)
-        if q_out.shape[0] != T:
-            raise ValueError("q_out must have q's shape")
-        q_args, out_args = (q.data_ptr(), qs), (q_out.data_ptr(), os)
-    axis_stride = positions.stride(0) if rope.num_axes > 1 else T
-    st = _launch(dev, stream, used, lambda s: _native.lib().paged_kv_rope_write(
-        *q_args, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-        axis_stride, slot_mapping.data_ptr(), T, Hq,
-        ctypes.byref(rope.c_struct()), ctypes.byref(cache.c_struct()),
-        *out_args, s))
+            q_out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=dev)
+            used = (q_out,)
+        To, os = _head_rows(q_out, "q_out", dev, Hq, d)
+        if Tq != T or To != T:
+            raise ValueError("q, q_out and k must name the same tokens")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    st = _launch(_native.lib().paged_kv_rope_write, (
+        qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+        stride[0] if A > 1 else T, slot_mapping.data_ptr(), T, Hq, rope.c_struct(),
+        cache.c_struct(), op, os), dev, stream, used)
     _native.check("paged_kv_rope_write", st)
     return q_out
 
@@ -651,17 +656,19 @@ def paged_attention_decode_weights(q: torch.Tensor, cache: PagedKVCache,
     weight becomes decay times itself plus its weight in this step, summed
     over the kv head's query heads; positions written by the call start
     from 0.  Returns out [B, Hq, d] bf16."""
-    dev = cache.device
+    key_cache = cache.key_cache
+    dev = key_cache.device
     _require(q, "q", torch.bfloat16, dev, 3)
     _require(block_tables, "block_tables", torch.int32, dev, 2)
     _require(seq_lens, "seq_lens", torch.int32, dev, 1)
     _require(weights, "weights", torch.float32, dev, 3)
     B, Hq, d = q.shape
-    Hkv = cache.num_kv_heads
-    if d != cache.head_dim or block_tables.shape[0] != B or \
-            seq_lens.shape[0] != B:
+    _, _, Hkv, d_cache = key_cache.shape
+    rows, max_blocks = block_tables.shape
+    if d != d_cache or rows != B or seq_lens.shape[0] != B:
         raise ValueError("q, block_tables, seq_lens shapes do not match")
-    if tuple(weights.shape[:2]) != (B, Hkv) or weights.shape[2] < max_seq_len:
+    w_rows, w_heads, width = weights.shape
+    if w_rows != B or w_heads != Hkv or width < max_seq_len:
         raise ValueError(f"weights must be [{B}, {Hkv}, >= {max_seq_len}]")
     used = []
     if out is None:
@@ -694,12 +701,11 @@ def paged_attention_decode_weights(q: torch.Tensor, cache: PagedKVCache,
             dtype=torch.uint8, device=dev)
         used.append(workspace)
     _require(workspace, "workspace", torch.uint8, dev, 1)
-    st = _launch(dev, stream, used, lambda s: _native.lib().paged_attention_decode_weights(
-        q.data_ptr(), *new, ctypes.byref(cache.c_struct()),
-        block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-        B, Hq, float(scale), out.data_ptr(), weights.data_ptr(),
-        weights.shape[2], float(decay), int(max_seq_len),
-        int(partition_tokens), workspace.data_ptr(), workspace.numel(), s))
+    st = _launch(_native.lib().paged_attention_decode_weights, (
+        q.data_ptr(), *new, cache.c_struct(), block_tables.data_ptr(), max_blocks,
+        seq_lens.data_ptr(), B, Hq, scale, out.data_ptr(), weights.data_ptr(),
+        width, decay, max_seq_len, partition_tokens, workspace.data_ptr(),
+        workspace.numel()), dev, stream, used)
     _native.check("paged_attention_decode_weights", st)
     return out
 
@@ -732,32 +738,35 @@ def paged_kv_evict(cache: PagedKVCache, block_tables: torch.Tensor,
     max_keep bounds the lengths left.  kept (int32 [B, num_kv_heads or 1,
     max_keep]), when given, receives the old positions, -1 past n.  Returns
     new_seq_lens int32 [B] (which may be seq_lens, to update it)."""
-    dev = cache.device
-    max_keep = int(max_keep)
+    key_cache = cache.key_cache
+    dev = key_cache.device
     _require(block_tables, "block_tables", torch.int32, dev, 2)
     _require(seq_lens, "seq_lens", torch.int32, dev, 1)
     _require(weights, "weights", torch.float32, dev, 3)
     _require(keep, "keep", torch.int32, dev, 1)
-    B, Hkv = seq_lens.shape[0], cache.num_kv_heads
-    if block_tables.shape[0] != B or keep.shape[0] != B or \
-            tuple(weights.shape[:2]) != (B, Hkv):
+    Hkv = key_cache.shape[2]
+    rows, max_blocks = block_tables.shape
+    B, w_heads, width = weights.shape
+    if rows != B or seq_lens.shape[0] != B or keep.shape[0] != B or w_heads != Hkv:
         raise ValueError("block_tables, seq_lens, weights, keep shapes do not match")
     dst, dst_blocks, dst_w, dst_stride, kept_ptr = None, 0, None, 0, None
     if dst_tables is not None:
         _require(dst_tables, "dst_tables", torch.int32, dev, 2)
-        if dst_tables.shape[0] != B or dst_tables.shape[1] < 1:
+        rows, dst_blocks = dst_tables.shape
+        if rows != B or dst_blocks < 1:
             raise ValueError("dst_tables must have a row of blocks per sequence")
-        dst, dst_blocks = dst_tables.data_ptr(), dst_tables.shape[1]
+        dst = dst_tables.data_ptr()
     if dst_weights is not None:
         _require(dst_weights, "dst_weights", torch.float32, dev, 3)
-        if tuple(dst_weights.shape[:2]) != (B, Hkv) or dst_weights.shape[2] < 1:
+        rows, w_heads, dst_stride = dst_weights.shape
+        if rows != B or w_heads != Hkv or dst_stride < 1:
             raise ValueError(f"dst_weights must be [{B}, {Hkv}, >= 1]")
-        dst_w, dst_stride = dst_weights.data_ptr(), dst_weights.shape[2]
+        dst_w = dst_weights.data_ptr()
     if kept is not None:
         _require(kept, "kept", torch.int32, dev, 3)
-        shape = (B, Hkv if per_head else 1, max_keep)
-        if tuple(kept.shape) != shape:
-            raise ValueError(f"kept must have shape {shape}")
+        if kept.shape != (B, Hkv if per_head else 1, max_keep):
+            raise ValueError("kept must have shape "
+                             f"{(B, Hkv if per_head else 1, max_keep)}")
         kept_ptr = kept.data_ptr()
     used = []
     if new_seq_lens is None:
@@ -768,17 +777,16 @@ def paged_kv_evict(cache: PagedKVCache, block_tables: torch.Tensor,
         raise ValueError("new_seq_lens must have an entry per sequence")
     if workspace is None:
         workspace = torch.empty(
-            max(1, paged_kv_evict_workspace_bytes(B, Hkv, weights.shape[2], max_keep)),
+            max(1, paged_kv_evict_workspace_bytes(B, Hkv, width, max_keep)),
             dtype=torch.uint8, device=dev)
         used.append(workspace)
     _require(workspace, "workspace", torch.uint8, dev, 1)
-    st = _launch(dev, stream, used, lambda s: _native.lib().paged_kv_evict(
-        ctypes.byref(cache.c_struct()), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), weights.data_ptr(),
-        weights.shape[2], keep.data_ptr(), B, max_keep, int(sink),
-        int(recent), int(bool(per_head)), dst, dst_blocks, dst_w, dst_stride,
-        new_seq_lens.data_ptr(), kept_ptr, workspace.data_ptr(),
-        workspace.numel(), s))
+    st = _launch(_native.lib().paged_kv_evict, (
+        cache.c_struct(), block_tables.data_ptr(), max_blocks,
+        seq_lens.data_ptr(), weights.data_ptr(), width, keep.data_ptr(), B,
+        max_keep, sink, recent, bool(per_head), dst, dst_blocks, dst_w,
+        dst_stride, new_seq_lens.data_ptr(), kept_ptr, workspace.data_ptr(),
+        workspace.numel()), dev, stream, used)
     _native.check("paged_kv_evict", st)
     return new_seq_lens
 
