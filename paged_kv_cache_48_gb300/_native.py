@@ -11,6 +11,7 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 LIBRARY = PKG / "libpagedkv.so"
+BINDING = PKG / "_binding.so"
 HEADER = PKG.parent / "include" / "pagedkv.h"
 HEADERS = sorted((PKG.parent / "include").glob("*.h"))
 
@@ -126,6 +127,7 @@ _SIGNATURES = {
 }
 
 _LIB = None
+_BINDING = None
 
 
 class PagedKVError(RuntimeError):
@@ -167,6 +169,21 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _LIB = handle
     return _LIB
+
+
+def binding():
+    """The native argument layer of the per-layer calls (csrc/binding.cpp);
+    raises if it has not been built."""
+    global _BINDING
+    if _BINDING is None:
+        lib()
+        if not BINDING.exists():
+            raise RuntimeError(
+                f"{BINDING} is missing: build it with "
+                "`python -m paged_kv_cache_48_gb300.build`")
+        from . import _binding
+        _BINDING = _binding
+    return _BINDING
 
 
 def check(call: str, status: int) -> None:

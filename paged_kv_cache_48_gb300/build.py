@@ -3,6 +3,8 @@
 Each CUDA translation unit compiles in parallel to an object under
 ``_build/``; the objects link into ``paged_kv_cache_48_gb300/libpagedkv.so``.
 No relocatable device code, a single ``-gencode`` target (sm_103a).
+``csrc/binding.cpp`` (argument checks of the per-layer calls, against torch's
+headers) becomes ``_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -17,6 +20,7 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 BUILD = PKG / "_build"
 LIBRARY = PKG / "libpagedkv.so"
+BINDING = PKG / "_binding.so"
 SOURCES = ["kv_write_zero.cu", "attention_decode.cu", "pkv_api.cu",
            "attention_noalloc.cu", "kv_blocks.cu", "input_prep.cu",
            "attention_prefill.cu", "rope_write.cu", "kv_evict.cu"]
@@ -33,6 +37,11 @@ def _nvcc() -> str:
         return cand
     home = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     return str(Path(home) / "bin" / "nvcc")
+
+
+def _torch_dir() -> Path:
+    import importlib.util
+    return Path(importlib.util.find_spec("torch").origin).parent
 
 
 def _stale(target: Path, deps) -> bool:
@@ -61,8 +70,25 @@ def build(verbose: bool = False, force: bool = False,
             subprocess.run(cmd, check=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = _torch_dir()
+
+    def compile_binding() -> Path:
+        src, obj = CSRC / "binding.cpp", BUILD / "binding.o"
+        # (torch's version header: another torch, another build)
+        if force or _stale(obj, [src, *header_deps, torch_dir / "version.py"]):
+            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+                   "-isystem", str(torch_dir / "include"),
+                   "-isystem", str(torch_dir / "include/torch/csrc/api/include"),
+                   "-isystem", sysconfig.get_path("include"), "-c", str(src), "-o", str(obj)]
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            subprocess.run(cmd, check=True)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     if force or _stale(LIBRARY, objs):
         tmp = LIBRARY.with_name(LIBRARY.name + f".tmp{os.getpid()}")
         cmd = [nvcc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
@@ -70,6 +96,15 @@ def build(verbose: bool = False, force: bool = False,
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIBRARY)
+    if force or _stale(BINDING, [binding_obj, LIBRARY]):
+        tmp = BINDING.with_name(BINDING.name + f".tmp{os.getpid()}")
+        cmd = ["g++", "-shared", "-o", str(tmp), str(binding_obj), "-L", str(PKG),
+               f"-l:{LIBRARY.name}", "-L", str(torch_dir / "lib"), "-ltorch_python",
+               "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, BINDING)
     return LIBRARY
 
 

@@ -1,0 +1,291 @@
+// binding.cpp -- CPython entry points of the calls that a step makes once per
+// layer with many tensors: the rotary write, decode attention with running
+// weights, eviction.  Argument checks and marshalling only, as ops.py does for
+// the other calls, but reading dtype, shape, strides and pointers of a tensor
+// natively: a call of ten tensors costs the host a few hundred nanoseconds
+// instead of 5 to 8 us of attribute reads.  Wrong types raise TypeError, wrong
+// shapes or devices ValueError; the C ABI's status is returned.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/pagedkv.h"
+
+namespace {
+
+struct Raised {};  // a Python exception is set
+
+[[noreturn]] void fail(PyObject *type, const char *fmt, ...) {
+  char msg[320];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof msg, fmt, ap);
+  va_end(ap);
+  PyErr_SetString(type, msg);
+  throw Raised();
+}
+
+const at::Tensor &tensor(PyObject *o, const char *name) {
+  if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a torch.Tensor", name);
+  return THPVariable_Unpack(o);
+}
+
+// dtype, device and number of dimensions; contiguity unless the caller reads
+// the strides itself.
+const at::Tensor &checked(PyObject *o, const char *name, at::ScalarType dtype, int device, int ndim,
+                          bool contiguous = true) {
+  const at::Tensor &t = tensor(o, name);
+  if (t.scalar_type() != dtype)
+    fail(PyExc_TypeError, "%s must be %s, got %s", name, c10::toString(dtype),
+         c10::toString(t.scalar_type()));
+  if (!t.device().is_cuda() || t.device().index() != device)
+    fail(PyExc_ValueError, "%s must be on cuda:%d, got %s", name, device,
+         t.device().str().c_str());
+  if (t.dim() != ndim)
+    fail(PyExc_ValueError, "%s must have %d dims, got %d", name, ndim, (int)t.dim());
+  if (contiguous && !t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
+  return t;
+}
+
+int64_t integer(PyObject *o, const char *name, int64_t lo, int64_t hi) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised();
+  if (v < lo || v > hi) fail(PyExc_ValueError, "%s is out of range", name);
+  return v;
+}
+
+int32_t int32(PyObject *o, const char *name) {
+  return (int32_t)integer(o, name, INT32_MIN, INT32_MAX);
+}
+
+float real(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return (float)v;
+}
+
+void *address(PyObject *o) {
+  void *p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw Raised();
+  return p;
+}
+
+template <typename F>
+PyObject *call(Py_ssize_t n, Py_ssize_t want, F f) {
+  try {
+    if (n != want) fail(PyExc_TypeError, "expected %d arguments, got %d", (int)want, (int)n);
+    return PyLong_FromLong((long)f());
+  } catch (const Raised &) {
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+template <typename F>
+pkv_status without_gil(F f) {
+  PyThreadState *state = PyEval_SaveThread();
+  const pkv_status st = f();  // (the C ABI throws nothing)
+  PyEval_RestoreThread(state);
+  return st;
+}
+
+// [T, heads, dim] bf16 rows whose heads are contiguous.
+struct Rows {
+  void *data = nullptr;
+  int64_t tokens = 0, stride = 0, heads = 0;
+};
+
+Rows head_rows(PyObject *o, const char *name, int device, int64_t heads, int64_t dim) {
+  const at::Tensor &t = checked(o, name, at::kBFloat16, device, 3, false);
+  Rows r;
+  r.tokens = t.size(0);
+  r.heads = t.size(1);
+  if ((heads >= 0 && r.heads != heads) || t.size(2) != dim)
+    fail(PyExc_ValueError, "%s must be [T, %lld, %lld], got [%lld, %lld, %lld]", name,
+         (long long)(heads >= 0 ? heads : r.heads), (long long)dim, (long long)r.tokens,
+         (long long)r.heads, (long long)t.size(2));
+  if (t.stride(2) != 1 || (t.stride(1) != dim && r.heads > 1))
+    fail(PyExc_ValueError, "%s: a token's heads must be contiguous", name);
+  r.stride = r.tokens > 1 ? t.stride(0) : r.heads * dim;
+  r.data = t.data_ptr();
+  return r;
+}
+
+// (q | None, k, v, positions, slot_mapping, cache, device, rope, q_out | None,
+// stream): cache and rope are addresses of a pkv_cache and a pkv_rope.
+PyObject *rope_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 10, [&] {
+    const int device = int32(a[6], "device");
+    const pkv_cache *cache = static_cast<const pkv_cache *>(address(a[5]));
+    const pkv_rope *rope = static_cast<const pkv_rope *>(address(a[7]));
+    const int64_t dim = cache->head_dim;
+    const Rows k = head_rows(a[1], "k", device, cache->num_kv_heads, dim);
+    const Rows v = head_rows(a[2], "v", device, cache->num_kv_heads, dim);
+    const at::Tensor &slots = checked(a[4], "slot_mapping", at::kLong, device, 1);
+    if (v.tokens != k.tokens || slots.size(0) != k.tokens)
+      fail(PyExc_ValueError, "k, v, slot_mapping must name the same tokens");
+    const int64_t T = k.tokens, A = rope->num_axes;
+    const int dims = (int)tensor(a[3], "positions").dim();
+    const at::Tensor &pos = checked(a[3], "positions", at::kInt, device, dims, false);
+    const bool flat = dims == 1 && A == 1;
+    if ((!flat && (dims != 2 || pos.size(0) != A)) || pos.size(dims - 1) != T ||
+        (T > 1 && pos.stride(dims - 1) != 1))
+      fail(PyExc_ValueError, "positions must be [%lld, %lld] with contiguous rows", (long long)A,
+           (long long)T);
+    Rows q, out;
+    if (a[0] != Py_None) {
+      q = head_rows(a[0], "q", device, -1, dim);
+      out = head_rows(a[8], "q_out", device, q.heads, dim);
+      if (q.tokens != T || out.tokens != T)
+        fail(PyExc_ValueError, "q, q_out and k must name the same tokens");
+    } else if (a[8] != Py_None) {
+      fail(PyExc_ValueError, "q_out without q");
+    }
+    if (q.heads > INT32_MAX) fail(PyExc_ValueError, "q has too many heads");
+    void *stream = address(a[9]);
+    return without_gil([&] {
+      return paged_kv_rope_write(q.data, q.stride, k.data, k.stride, v.data, v.stride,
+                                 static_cast<const int32_t *>(pos.data_ptr()),
+                                 A > 1 ? pos.stride(0) : T,
+                                 static_cast<const int64_t *>(slots.data_ptr()), T,
+                                 (int32_t)q.heads, rope, cache, out.data, out.stride, stream);
+    });
+  });
+}
+
+// (q, k_new | None, v_new | None, new_start_loc | None, cache, device,
+// block_tables, seq_lens, scale, out, weights, decay, max_seq_len,
+// partition_tokens, workspace, stream)
+PyObject *decode_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 16, [&] {
+    const int device = int32(a[5], "device");
+    const pkv_cache *cache = static_cast<const pkv_cache *>(address(a[4]));
+    const at::Tensor &q = checked(a[0], "q", at::kBFloat16, device, 3);
+    const at::Tensor &tables = checked(a[6], "block_tables", at::kInt, device, 2);
+    const at::Tensor &lens = checked(a[7], "seq_lens", at::kInt, device, 1);
+    const at::Tensor &out = checked(a[9], "out", at::kBFloat16, device, 3);
+    const at::Tensor &w = checked(a[10], "weights", at::kFloat, device, 3);
+    const int64_t B = q.size(0), heads = q.size(1), dim = q.size(2), kv = cache->num_kv_heads;
+    const int32_t max_len = int32(a[12], "max_seq_len"), pt = int32(a[13], "partition_tokens");
+    if (dim != cache->head_dim || tables.size(0) != B || lens.size(0) != B)
+      fail(PyExc_ValueError, "q, block_tables, seq_lens shapes do not match");
+    if (w.size(0) != B || w.size(1) != kv || w.size(2) < max_len)
+      fail(PyExc_ValueError, "weights must be [%lld, %lld, >= %d]", (long long)B, (long long)kv,
+           max_len);
+    if (out.sizes() != q.sizes()) fail(PyExc_ValueError, "out must have q's shape");
+    void *kn = nullptr, *vn = nullptr, *start = nullptr;
+    int64_t n_new = 0;
+    if (a[1] != Py_None || a[2] != Py_None || a[3] != Py_None) {
+      const at::Tensor &k = checked(a[1], "k_new", at::kBFloat16, device, 3);
+      const at::Tensor &v = checked(a[2], "v_new", at::kBFloat16, device, 3);
+      n_new = k.size(0);
+      if (k.size(1) != kv || k.size(2) != dim || v.sizes() != k.sizes())
+        fail(PyExc_ValueError, "k_new and v_new must be [num_new, num_kv_heads, head_dim]");
+      if (a[3] != Py_None) {
+        const at::Tensor &s = checked(a[3], "new_start_loc", at::kInt, device, 1);
+        if (s.size(0) != B + 1) fail(PyExc_ValueError, "new_start_loc must be [batch + 1]");
+        start = s.data_ptr();
+      } else if (n_new != B) {
+        fail(PyExc_ValueError, "without new_start_loc, k_new holds one row per sequence");
+      }
+      kn = k.data_ptr();
+      vn = v.data_ptr();
+    }
+    if (B > INT32_MAX || heads > INT32_MAX || tables.size(1) > INT32_MAX)
+      fail(PyExc_ValueError, "q or block_tables is too large");
+    const at::Tensor &ws = checked(a[14], "workspace", at::kByte, device, 1);
+    const float scale = real(a[8]), decay = real(a[11]);
+    void *stream = address(a[15]);
+    return without_gil([&] {
+      return paged_attention_decode_weights(
+          q.data_ptr(), kn, vn, static_cast<const int32_t *>(start), n_new, cache,
+          static_cast<const int32_t *>(tables.data_ptr()), (int32_t)tables.size(1),
+          static_cast<const int32_t *>(lens.data_ptr()), (int32_t)B, (int32_t)heads, scale,
+          out.data_ptr(), static_cast<float *>(w.data_ptr()), w.size(2), decay, max_len, pt,
+          ws.data_ptr(), (size_t)ws.numel(), stream);
+    });
+  });
+}
+
+// (cache, device, block_tables, seq_lens, weights, keep, max_keep, sink,
+// recent, per_head, dst_tables | None, dst_weights | None, new_seq_lens,
+// kept | None, workspace, stream)
+PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return call(n, 16, [&] {
+    const int device = int32(a[1], "device");
+    const pkv_cache *cache = static_cast<const pkv_cache *>(address(a[0]));
+    const at::Tensor &tables = checked(a[2], "block_tables", at::kInt, device, 2);
+    const at::Tensor &lens = checked(a[3], "seq_lens", at::kInt, device, 1);
+    const at::Tensor &w = checked(a[4], "weights", at::kFloat, device, 3);
+    const at::Tensor &keep = checked(a[5], "keep", at::kInt, device, 1);
+    const int32_t max_keep = int32(a[6], "max_keep"), sink = int32(a[7], "sink");
+    const int32_t recent = int32(a[8], "recent");
+    const int per_head = PyObject_IsTrue(a[9]);
+    if (per_head < 0) throw Raised();
+    const int64_t B = w.size(0), kv = cache->num_kv_heads;
+    if (tables.size(0) != B || lens.size(0) != B || keep.size(0) != B || w.size(1) != kv)
+      fail(PyExc_ValueError, "block_tables, seq_lens, weights, keep shapes do not match");
+    void *dst = nullptr, *kept = nullptr;
+    float *dst_w = nullptr;
+    int64_t dst_blocks = 0, dst_stride = 0;
+    if (a[10] != Py_None) {
+      const at::Tensor &t = checked(a[10], "dst_tables", at::kInt, device, 2);
+      dst_blocks = t.size(1);
+      if (t.size(0) != B || dst_blocks < 1)
+        fail(PyExc_ValueError, "dst_tables must have a row of blocks per sequence");
+      dst = t.data_ptr();
+    }
+    if (a[11] != Py_None) {
+      const at::Tensor &t = checked(a[11], "dst_weights", at::kFloat, device, 3);
+      dst_stride = t.size(2);
+      if (t.size(0) != B || t.size(1) != kv || dst_stride < 1)
+        fail(PyExc_ValueError, "dst_weights must be [%lld, %lld, >= 1]", (long long)B,
+             (long long)kv);
+      dst_w = static_cast<float *>(t.data_ptr());
+    }
+    const at::Tensor &new_lens = checked(a[12], "new_seq_lens", at::kInt, device, 1);
+    if (new_lens.size(0) != B)
+      fail(PyExc_ValueError, "new_seq_lens must have an entry per sequence");
+    if (a[13] != Py_None) {
+      const at::Tensor &t = checked(a[13], "kept", at::kInt, device, 3);
+      if (t.size(0) != B || t.size(1) != (per_head ? kv : 1) || t.size(2) != max_keep)
+        fail(PyExc_ValueError, "kept must have shape [%lld, %lld, %d]", (long long)B,
+             (long long)(per_head ? kv : 1), max_keep);
+      kept = t.data_ptr();
+    }
+    if (B > INT32_MAX || tables.size(1) > INT32_MAX || dst_blocks > INT32_MAX)
+      fail(PyExc_ValueError, "block_tables or dst_tables is too large");
+    const at::Tensor &ws = checked(a[14], "workspace", at::kByte, device, 1);
+    void *stream = address(a[15]);
+    return without_gil([&] {
+      return paged_kv_evict(
+          cache, static_cast<const int32_t *>(tables.data_ptr()), (int32_t)tables.size(1),
+          static_cast<const int32_t *>(lens.data_ptr()), static_cast<float *>(w.data_ptr()),
+          w.size(2), static_cast<const int32_t *>(keep.data_ptr()), (int32_t)B, max_keep, sink,
+          recent, per_head, static_cast<const int32_t *>(dst), (int32_t)dst_blocks, dst_w,
+          dst_stride, static_cast<int32_t *>(new_lens.data_ptr()), static_cast<int32_t *>(kept),
+          ws.data_ptr(), (size_t)ws.numel(), stream);
+    });
+  });
+}
+
+PyMethodDef methods[] = {
+    {"rope_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_write)),
+     METH_FASTCALL, nullptr},
+    {"decode_weights", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_weights)),
+     METH_FASTCALL, nullptr},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict)), METH_FASTCALL,
+     nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }

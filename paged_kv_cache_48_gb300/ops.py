@@ -2,7 +2,9 @@
 
 Marshalling only: tensors are checked for dtype, shape, device and
 contiguity, their data pointers and torch's current CUDA stream are passed
-to ``libpagedkv.so``, and a non-OK status raises ``PagedKVError``.  Every
+to ``libpagedkv.so``, and a non-OK status raises ``PagedKVError``.  The
+per-layer calls with many tensors (rotary write, decode with running
+weights, eviction) have their checks in ``csrc/binding.cpp``.  Every
 step of the path (write, zeroing, gather, attention, reduce) runs in the
 library's kernels; PyTorch only owns the device memory and the streams.
 """
@@ -68,6 +70,7 @@ class PagedKVCache:
             key_cache.data_ptr(), value_cache.data_ptr(), key_cache.shape[0],
             BLOCK_SIZE, key_cache.shape[2], key_cache.shape[3],
             _DTYPES[kv_dtype], self.k_scale, self.v_scale)
+        self.c_address = ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, num_blocks: int, num_kv_heads: int, head_dim: int,
@@ -529,15 +532,17 @@ class RotaryAxes:
         self.interleave_pairs = bool(interleave_pairs)
         self._struct = PkvRope(self.frequencies.ctypes.data, self.axis.ctypes.data, A,
                                rotary_dim, int(self.interleave_pairs))
+        self.c_address = ctypes.addressof(self._struct)
 
     def c_struct(self) -> PkvRope:
         return self._struct
 
 
 def _launch(fn, args, dev: torch.device, stream: Optional[torch.cuda.Stream], used) -> int:
-    """fn(*args, stream handle) with `dev` current.  `used` are tensors this
-    module allocated for the call: on a stream other than torch's current
-    one, the allocator is told that they are in use there."""
+    """fn(*args, stream handle) with `dev` current, fn a function of the native
+    binding.  `used` are tensors this module allocated for the call: on a
+    stream other than torch's current one, the allocator is told that they
+    are in use there."""
     if stream is None:
         handle = _raw_stream(dev.index)
     else:
@@ -558,24 +563,6 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _head_rows(t: torch.Tensor, name: str, dev, heads: int, dim: int):
-    """(tokens, token stride in elements) of [T, heads, dim] bf16 rows whose
-    heads are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
-    token, head, element = t.stride()
-    if element != 1 or (head != dim and heads > 1):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return shape[0], token if shape[0] > 1 else heads * dim
-
-
 def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
                         v: torch.Tensor, positions: torch.Tensor,
                         slot_mapping: torch.Tensor, cache: PagedKVCache,
@@ -587,43 +574,16 @@ def paged_kv_rope_write(q: Optional[torch.Tensor], k: torch.Tensor,
     q [T, Hq, d], k and v [T, num_kv_heads, d] bf16 may be slices of one
     projection's output (a token's heads contiguous).  Returns q_out (q
     itself turns q in place; None with q None)."""
-    key_cache = cache.key_cache
-    dev = key_cache.device
-    _, _, Hkv, d = key_cache.shape
-    T, ks = _head_rows(k, "k", dev, Hkv, d)
-    Tv, vs = _head_rows(v, "v", dev, Hkv, d)
-    _require(slot_mapping, "slot_mapping", torch.int64, dev, 1)
+    dev = cache.key_cache.device
     if not isinstance(rope, RotaryAxes):
         raise TypeError("rope must be a RotaryAxes")
-    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
-        raise TypeError(f"positions must be a tensor of {torch.int32}")
-    if positions.device != dev:
-        raise ValueError(f"positions must be on {dev}, got {positions.device}")
-    A = rope.num_axes
-    shape, stride = positions.shape, positions.stride()
-    if not (shape == (A, T) or (A == 1 and shape == (T,))) or (T > 1 and stride[-1] != 1):
-        raise ValueError(f"positions must be [{A}, {T}] with contiguous rows")
-    if Tv != T or slot_mapping.shape[0] != T:
-        raise ValueError("k, v, slot_mapping must name the same tokens")
     used = ()
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        Hq, qp, qs, op, os = 0, None, 0, None, 0
-    else:
-        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        Tq, qs = _head_rows(q, "q", dev, Hq, d)
-        if q_out is None:
-            q_out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=dev)
-            used = (q_out,)
-        To, os = _head_rows(q_out, "q_out", dev, Hq, d)
-        if Tq != T or To != T:
-            raise ValueError("q, q_out and k must name the same tokens")
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    st = _launch(_native.lib().paged_kv_rope_write, (
-        qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-        stride[0] if A > 1 else T, slot_mapping.data_ptr(), T, Hq, rope.c_struct(),
-        cache.c_struct(), op, os), dev, stream, used)
+    if q_out is None and q is not None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        used = (q_out,)
+    st = _launch(_native.binding().rope_write, (
+        q, k, v, positions, slot_mapping, cache.c_address, dev.index,
+        rope.c_address, q_out), dev, stream, used)
     _native.check("paged_kv_rope_write", st)
     return q_out
 
@@ -656,56 +616,21 @@ def paged_attention_decode_weights(q: torch.Tensor, cache: PagedKVCache,
     weight becomes decay times itself plus its weight in this step, summed
     over the kv head's query heads; positions written by the call start
     from 0.  Returns out [B, Hq, d] bf16."""
-    key_cache = cache.key_cache
-    dev = key_cache.device
-    _require(q, "q", torch.bfloat16, dev, 3)
-    _require(block_tables, "block_tables", torch.int32, dev, 2)
-    _require(seq_lens, "seq_lens", torch.int32, dev, 1)
-    _require(weights, "weights", torch.float32, dev, 3)
-    B, Hq, d = q.shape
-    _, _, Hkv, d_cache = key_cache.shape
-    rows, max_blocks = block_tables.shape
-    if d != d_cache or rows != B or seq_lens.shape[0] != B:
-        raise ValueError("q, block_tables, seq_lens shapes do not match")
-    w_rows, w_heads, width = weights.shape
-    if w_rows != B or w_heads != Hkv or width < max_seq_len:
-        raise ValueError(f"weights must be [{B}, {Hkv}, >= {max_seq_len}]")
+    dev = cache.key_cache.device
     used = []
     if out is None:
         out = torch.empty_like(q)
         used.append(out)
-    else:
-        _require(out, "out", torch.bfloat16, dev, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    new = (None, None, None, 0)
-    if k_new is not None or v_new is not None or new_start_loc is not None:
-        n_new = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else -1
-        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-            _require(t, n, torch.bfloat16, dev, 3)
-            if t.shape != (n_new, Hkv, d):
-                raise ValueError(f"{n} must be [num_new, num_kv_heads, head_dim]")
-        nsl = None
-        if new_start_loc is not None:
-            _require(new_start_loc, "new_start_loc", torch.int32, dev, 1)
-            if new_start_loc.shape[0] != B + 1:
-                raise ValueError("new_start_loc must be [batch + 1]")
-            nsl = new_start_loc.data_ptr()
-        elif n_new != B:
-            raise ValueError("without new_start_loc, k_new holds one row per sequence")
-        new = (k_new.data_ptr(), v_new.data_ptr(), nsl, n_new)
     if workspace is None:
         workspace = torch.empty(
             max(1, paged_attention_decode_weights_workspace_bytes(
-                B, Hq, Hkv, d, max_seq_len, partition_tokens)),
-            dtype=torch.uint8, device=dev)
+                q.shape[0], q.shape[1], cache.num_kv_heads, cache.head_dim,
+                max_seq_len, partition_tokens)), dtype=torch.uint8, device=dev)
         used.append(workspace)
-    _require(workspace, "workspace", torch.uint8, dev, 1)
-    st = _launch(_native.lib().paged_attention_decode_weights, (
-        q.data_ptr(), *new, cache.c_struct(), block_tables.data_ptr(), max_blocks,
-        seq_lens.data_ptr(), B, Hq, scale, out.data_ptr(), weights.data_ptr(),
-        width, decay, max_seq_len, partition_tokens, workspace.data_ptr(),
-        workspace.numel()), dev, stream, used)
+    st = _launch(_native.binding().decode_weights, (
+        q, k_new, v_new, new_start_loc, cache.c_address, dev.index, block_tables,
+        seq_lens, scale, out, weights, decay, max_seq_len, partition_tokens,
+        workspace), dev, stream, used)
     _native.check("paged_attention_decode_weights", st)
     return out
 
@@ -738,55 +663,21 @@ def paged_kv_evict(cache: PagedKVCache, block_tables: torch.Tensor,
     max_keep bounds the lengths left.  kept (int32 [B, num_kv_heads or 1,
     max_keep]), when given, receives the old positions, -1 past n.  Returns
     new_seq_lens int32 [B] (which may be seq_lens, to update it)."""
-    key_cache = cache.key_cache
-    dev = key_cache.device
-    _require(block_tables, "block_tables", torch.int32, dev, 2)
-    _require(seq_lens, "seq_lens", torch.int32, dev, 1)
-    _require(weights, "weights", torch.float32, dev, 3)
-    _require(keep, "keep", torch.int32, dev, 1)
-    Hkv = key_cache.shape[2]
-    rows, max_blocks = block_tables.shape
-    B, w_heads, width = weights.shape
-    if rows != B or seq_lens.shape[0] != B or keep.shape[0] != B or w_heads != Hkv:
-        raise ValueError("block_tables, seq_lens, weights, keep shapes do not match")
-    dst, dst_blocks, dst_w, dst_stride, kept_ptr = None, 0, None, 0, None
-    if dst_tables is not None:
-        _require(dst_tables, "dst_tables", torch.int32, dev, 2)
-        rows, dst_blocks = dst_tables.shape
-        if rows != B or dst_blocks < 1:
-            raise ValueError("dst_tables must have a row of blocks per sequence")
-        dst = dst_tables.data_ptr()
-    if dst_weights is not None:
-        _require(dst_weights, "dst_weights", torch.float32, dev, 3)
-        rows, w_heads, dst_stride = dst_weights.shape
-        if rows != B or w_heads != Hkv or dst_stride < 1:
-            raise ValueError(f"dst_weights must be [{B}, {Hkv}, >= 1]")
-        dst_w = dst_weights.data_ptr()
-    if kept is not None:
-        _require(kept, "kept", torch.int32, dev, 3)
-        if kept.shape != (B, Hkv if per_head else 1, max_keep):
-            raise ValueError("kept must have shape "
-                             f"{(B, Hkv if per_head else 1, max_keep)}")
-        kept_ptr = kept.data_ptr()
+    dev = cache.key_cache.device
     used = []
     if new_seq_lens is None:
         new_seq_lens = torch.empty_like(seq_lens)
         used.append(new_seq_lens)
-    _require(new_seq_lens, "new_seq_lens", torch.int32, dev, 1)
-    if new_seq_lens.shape[0] != B:
-        raise ValueError("new_seq_lens must have an entry per sequence")
     if workspace is None:
         workspace = torch.empty(
-            max(1, paged_kv_evict_workspace_bytes(B, Hkv, width, max_keep)),
+            max(1, paged_kv_evict_workspace_bytes(
+                seq_lens.shape[0], cache.num_kv_heads, weights.shape[2], max_keep)),
             dtype=torch.uint8, device=dev)
         used.append(workspace)
-    _require(workspace, "workspace", torch.uint8, dev, 1)
-    st = _launch(_native.lib().paged_kv_evict, (
-        cache.c_struct(), block_tables.data_ptr(), max_blocks,
-        seq_lens.data_ptr(), weights.data_ptr(), width, keep.data_ptr(), B,
-        max_keep, sink, recent, bool(per_head), dst, dst_blocks, dst_w,
-        dst_stride, new_seq_lens.data_ptr(), kept_ptr, workspace.data_ptr(),
-        workspace.numel()), dev, stream, used)
+    st = _launch(_native.binding().evict, (
+        cache.c_address, dev.index, block_tables, seq_lens, weights, keep,
+        max_keep, sink, recent, per_head, dst_tables, dst_weights, new_seq_lens,
+        kept, workspace), dev, stream, used)
     _native.check("paged_kv_evict", st)
     return new_seq_lens
 
