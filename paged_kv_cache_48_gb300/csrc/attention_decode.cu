@@ -114,7 +114,7 @@ struct DecodeParams {
   // Running attention weights (kernels with WEIGHTS): every score (log2
   // units, -inf where excluded) is kept in logits, unit (b, kv head, query
   // sub-group) by unit, [logit_tokens][logit_heads] each, until the row's
-  // softmax statistics are known; weights_accumulate_kernel then adds the
+  // softmax statistics are known; weights_finish_kernel then adds the
   // weights to weights [B, Hkv, weights_stride].
   float *logits;
   float *weights;
@@ -679,7 +679,7 @@ __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int blk, i
 // Decode kernel
 // ===========================================================================
 // WEIGHTS: every score is also kept in p.logits, and every row's (max, sum)
-// in p.part_ml, split or not, for weights_accumulate_kernel; and a NaN score
+// in p.part_ml, split or not, for weights_finish_kernel; and a NaN score
 // makes its row NaN, as the formula does (a NaN sum is carried through, also
 // past a maximum of -inf), where the other kernels write 0.
 template <bool FP8, int D, bool WEIGHTS = false, int NW = 4, int RING_KB = 64>
@@ -723,7 +723,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const bool wait_at_exit = p.defer_dep_wait && blockIdx.x == gridDim.x - 1 &&
                             blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
   if (!p.defer_dep_wait) grid_dependency_wait();
-  allow_dependent_launch();
+  // WEIGHTS: the finishing grid is large, and its waiting CTAs slow down the
+  // last wave when they start early (E4M3, batch 128: 263 -> 255 us a call
+  // when they launch after the stream below)
+  if (!WEIGHTS) allow_dependent_launch();
 
   // q does not depend on the sequence's extent: its loads go out first
   const int heads_here = min(8, p.group - qg * 8);
@@ -909,6 +912,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
   }
 
+  if (WEIGHTS) allow_dependent_launch();
+
   // ---- warp-owned partition: this warp's result, staged through its ring --
   st.reduce_l();
   float *o_s = reinterpret_cast<float *>(ring);  // this warp's ring, now idle
@@ -1027,13 +1032,11 @@ __device__ __forceinline__ float part_weight(float2 v, float M) {
 // reduced with shuffles; outputs accumulate partition by partition, in
 // partition order.
 template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodeParams p) {
+__device__ __forceinline__ void merge_rows(const DecodeParams &p, long long cta) {
   constexpr int KD = D / 32;
   constexpr int PRE = 4;  // partitions loaded before the row's count is known
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long row = cta * 8 + (threadIdx.x >> 5);
   if (row >= (long long)p.batch * p.num_heads) return;
   const float2 *ml = p.part_ml + (size_t)row * p.max_parts;
   const float *po = p.part_o + (size_t)row * p.max_parts * D + lane;
@@ -1117,6 +1120,13 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodePar
   for (int k = 0; k < KD; ++k) orow[32 * k] = __float2bfloat16_rn(acc[k] * inv);
 }
 
+template <int D>
+__global__ void __launch_bounds__(256) paged_decode_merge_kernel(const DecodeParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  merge_rows<D, false>(p, blockIdx.x);
+}
+
 // The same merge for sequences split into many partitions: one CTA of 8
 // warps per (sequence, query head) row.  The row's maximum M comes from a
 // block-wide reduction over its (m, l) pairs; the weights 2^(m_j - M) l_j go
@@ -1128,8 +1138,7 @@ constexpr int kMergeWideThreads = 256;
 constexpr int kMergeChunk = 2048;
 
 template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(kMergeWideThreads)
-paged_decode_merge_wide_kernel(const DecodeParams p) {
+__device__ __forceinline__ void merge_row_wide(const DecodeParams &p, long long row) {
   constexpr int NWM = kMergeWideThreads / 32;
   constexpr int LPP = D / 4;      // lanes per partition (float4 each)
   constexpr int PPW = 32 / LPP;   // partitions per warp step
@@ -1137,10 +1146,7 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
   __shared__ float w_s[kMergeChunk];
   __shared__ float red_s[NWM];
   __shared__ float4 acc_s[SLOTS][LPP];
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long row = blockIdx.x;
   const int b = (int)(row / p.num_heads);
   const int cap = min(p.max_blocks * 16, p.max_seq_len);
   const int L = clamp_len(__ldg(p.seq_lens + b), cap);
@@ -1234,27 +1240,40 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kMergeWideThreads)
+paged_decode_merge_wide_kernel(const DecodeParams p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  merge_row_wide<D, false>(p, blockIdx.x);
+}
+
 // ---------------------------------------------------------------------------
 // Running attention weights: weights[b, kvh, t] = decay * weights[b, kvh, t]
 // + sum over the kv head's query heads h of 2^(s_ht - M_h) / l_h, from the
 // kept scores s and each row's partition statistics (m_j, l_j), M = max m_j,
-// l = sum 2^(m_j - M) l_j.  A CTA takes kAccTokens tokens of one (sequence,
-// kv head); a thread owns its tokens, so every sum has a fixed order.
+// l = sum 2^(m_j - M) l_j.  A CTA takes a run of kAccTokens-token chunks of
+// one (sequence, kv head): the statistics once, then chunk by chunk all the
+// scores of a thread's tokens loaded before the first is used, so that what
+// bounds it is memory.  A thread owns its tokens and every sum has a fixed
+// order.
 // ---------------------------------------------------------------------------
 constexpr int kAccThreads = 256;
 constexpr int kAccPerThread = 4;
 constexpr int kAccTokens = kAccThreads * kAccPerThread;
+constexpr int kAccHeads = 128;  // heads whose statistics a pass holds
 
-__global__ void __launch_bounds__(kAccThreads) weights_accumulate_kernel(const DecodeParams p) {
-  __shared__ float2 stat[8];  // (M, 1 / l) of a sub-group's heads; (0, 0) when a row is empty
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int b = blockIdx.z, kvh = blockIdx.y;
+// HP: scores of a token in a unit (heads of a sub-group, rounded up to even).
+template <int HP>
+__device__ __forceinline__ void accumulate_weights(const DecodeParams &p, int b, int kvh, int t_begin,
+                                                   int t_end) {
+  __shared__ float2 stat[kAccHeads];  // (M, 1 / l); (0, 0) when a row is empty
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = min(p.max_blocks * 16, p.max_seq_len);
   const int L_in = __ldg(p.seq_lens + b);
   const int L = clamp_len(L_in, cap);
-  const int t0 = blockIdx.x * kAccTokens;
-  if (t0 >= L) return;
+  if (t_begin >= L) return;
+  t_end = min(t_end, L);
   const int nparts = L <= p.part_tokens ? 1 : (L + p.part_tokens - 1) / p.part_tokens;
   // positions written by this call start from 0, whatever the row holds
   int fresh = L;
@@ -1268,56 +1287,98 @@ __global__ void __launch_bounds__(kAccThreads) weights_accumulate_kernel(const D
     }
     if (ok) fresh = L - n_new;
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int HP = p.logit_heads;
-  float acc[kAccPerThread];
-#pragma unroll
-  for (int k = 0; k < kAccPerThread; ++k) acc[k] = 0.f;
-  for (int qg = 0; qg < p.q_groups; ++qg) {
-    const int heads = min(8, p.group - qg * 8);
-    if (warp < heads) {
-      const size_t row = (size_t)b * p.num_heads + (size_t)kvh * p.group + qg * 8 + warp;
+  float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
+  for (int h0 = 0; h0 < p.group; h0 += kAccHeads) {  // (one pass up to 128 heads a kv head)
+    const int pass_heads = min(kAccHeads, p.group - h0);
+    for (int h = warp; h < pass_heads; h += kAccThreads / 32) {
+      const size_t row = (size_t)b * p.num_heads + (size_t)kvh * p.group + h0 + h;
       const float2 *ml = p.part_ml + row * p.max_parts;
-      float M = -INFINITY, l = 0.f;
-      for (int j = lane; j < nparts; j += 32) M = fmaxf(M, ml[j].x);
+      const float2 mine = lane < nparts ? ml[lane] : make_float2(-INFINITY, 0.f);
+      float M = mine.x, l = 0.f;
+      for (int j = lane + 32; j < nparts; j += 32) M = fmaxf(M, ml[j].x);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      for (int j = lane; j < nparts; j += 32) {
-        const float2 v = ml[j];
-        l += part_weight<true>(v, M);
-      }
+      l = part_weight<true>(mine, M);
+      for (int j = lane + 32; j < nparts; j += 32) l += part_weight<true>(ml[j], M);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-      if (lane == 0) stat[warp] = l != 0.f ? make_float2(M, 1.f / l) : make_float2(0.f, 0.f);
+      if (lane == 0) stat[h] = l != 0.f ? make_float2(M, 1.f / l) : make_float2(0.f, 0.f);
     }
     __syncthreads();
-    const float *lg = p.logits + (((size_t)b * p.num_kv_heads + kvh) * p.q_groups + qg) *
-                                     p.logit_tokens * HP;
+    const float decay = h0 == 0 ? p.decay : 1.f;
+    const int keep_below = h0 == 0 ? fresh : L;
+    const float *lg0 = p.logits + (((size_t)b * p.num_kv_heads + kvh) * p.q_groups + h0 / 8) *
+                                      p.logit_tokens * HP;
+    for (int t0 = t_begin; t0 < t_end; t0 += kAccTokens) {
+      float acc[kAccPerThread], old[kAccPerThread];
 #pragma unroll
-    for (int k = 0; k < kAccPerThread; ++k) {
-      const int t = t0 + k * kAccThreads + threadIdx.x;
-      if (t >= L) continue;
-      const float2 *row = reinterpret_cast<const float2 *>(lg + (size_t)t * HP);
-      for (int h = 0; h < heads; h += 2) {
-        const float2 s = __ldcs(row + h / 2);
-        const float2 a = stat[h];
-        if (a.y != 0.f) acc[k] += exp2f(s.x - a.x) * a.y;
-        if (h + 1 < heads) {
-          const float2 c = stat[h + 1];
-          if (c.y != 0.f) acc[k] += exp2f(s.y - c.x) * c.y;
+      for (int k = 0; k < kAccPerThread; ++k) {
+        const int t = t0 + k * kAccThreads + threadIdx.x;
+        acc[k] = 0.f;
+        old[k] = (decay != 0.f && t < min(t_end, keep_below)) ? w[t] : 0.f;
+      }
+      for (int g0 = 0; g0 < pass_heads; g0 += 8) {
+        const int heads = min(8, pass_heads - g0);
+        const float *lg = lg0 + (size_t)(g0 / 8) * p.logit_tokens * HP;
+        float s[kAccPerThread][HP];
+#pragma unroll
+        for (int k = 0; k < kAccPerThread; ++k) {
+          const int t = t0 + k * kAccThreads + threadIdx.x;
+#pragma unroll
+          for (int h = 0; h < HP; ++h) s[k][h] = -INFINITY;
+          if (t >= t_end) continue;
+          if constexpr (HP % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < HP; h += 4) {
+              const float4 v = __ldcs(reinterpret_cast<const float4 *>(lg + (size_t)t * HP + h));
+              s[k][h] = v.x, s[k][h + 1] = v.y, s[k][h + 2] = v.z, s[k][h + 3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < HP; h += 2) {
+              const float2 v = __ldcs(reinterpret_cast<const float2 *>(lg + (size_t)t * HP + h));
+              s[k][h] = v.x, s[k][h + 1] = v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float2 a = h < heads ? stat[g0 + h] : make_float2(0.f, 0.f);
+          if (a.y == 0.f) continue;  // (the same in every thread)
+#pragma unroll
+          for (int k = 0; k < kAccPerThread; ++k) acc[k] += exp2f(s[k][h] - a.x) * a.y;
         }
       }
-    }
-    __syncthreads();  // stat is reused by the next sub-group
-  }
-  float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
 #pragma unroll
-  for (int k = 0; k < kAccPerThread; ++k) {
-    const int t = t0 + k * kAccThreads + threadIdx.x;
-    if (t >= L) continue;
-    const float old = (p.decay != 0.f && t < fresh) ? p.decay * w[t] : 0.f;
-    w[t] = old + acc[k];
+      for (int k = 0; k < kAccPerThread; ++k) {
+        const int t = t0 + k * kAccThreads + threadIdx.x;
+        if (t < t_end) w[t] = (decay != 0.f ? decay * old[k] : 0.f) + acc[k];
+      }
+    }
+    __syncthreads();  // stat is reused by the next pass
   }
+}
+
+// The second launch of the decode with running weights: CTAs 0 .. merge_ctas
+// - 1 merge the split rows' outputs (as the merge kernels do), the others
+// take the `runs` runs of run_tokens tokens of each (sequence, kv head).  The
+// two only need the decode kernel's results, so they run side by side.
+template <int D, bool WIDE, int HP>
+__global__ void __launch_bounds__(kAccThreads)
+    weights_finish_kernel(const DecodeParams p, int merge_ctas, int runs, int run_tokens) {
+  static_assert(kAccThreads == kMergeWideThreads && kAccThreads == 256, "one block size for both");
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if ((int)blockIdx.x < merge_ctas) {
+    if constexpr (WIDE)
+      merge_row_wide<D, true>(p, blockIdx.x);
+    else
+      merge_rows<D, true>(p, blockIdx.x);
+    return;
+  }
+  const int i = blockIdx.x - merge_ctas, unit = i / runs;
+  const int t0 = (i - unit * runs) * run_tokens;
+  accumulate_weights<HP>(p, unit / p.num_kv_heads, unit % p.num_kv_heads, t0, t0 + run_tokens);
 }
 
 // ---------------------------------------------------------------------------
@@ -1464,6 +1525,42 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+template <int D, bool WIDE>
+cudaError_t launch_finish(const DecodeParams &p, int merge_ctas, int runs, int run_tokens,
+                          unsigned grid, cudaStream_t s) {
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(grid), dim3(kAccThreads), 0, s, p, merge_ctas, runs, run_tokens);
+  };
+  switch (p.logit_heads) {
+    case 2: return go(weights_finish_kernel<D, WIDE, 2>);
+    case 4: return go(weights_finish_kernel<D, WIDE, 4>);
+    case 6: return go(weights_finish_kernel<D, WIDE, 6>);
+    default: return go(weights_finish_kernel<D, WIDE, 8>);
+  }
+}
+
+template <int D>
+pkv_status launch_weights_finish(const DecodeParams &p, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.batch * p.num_heads;
+  const bool wide = p.max_parts > kMergeWarpMaxParts;
+  const int64_t merge = p.max_parts > 1 ? (wide ? rows : (rows + 7) / 8) : 0;
+  // runs of whole chunks, as long as still leaves eight CTAs an SM if every
+  // sequence had the bound's length
+  const int64_t chunks = ((int64_t)p.max_seq_len + kAccTokens - 1) / kAccTokens;
+  const int64_t units = (int64_t)p.num_kv_heads * p.batch;
+  const int64_t per_run = std::max<int64_t>(1, chunks * units / ((int64_t)device_sm_count() * 8));
+  const int64_t runs = (chunks + per_run - 1) / per_run;
+  const int64_t grid = merge + runs * units;
+  if (grid == 0) return PKV_OK;  // (a bound of 0: every length is 0)
+  if (grid > INT32_MAX) return PKV_ERR_ARG;
+  const int run_tokens = (int)(std::min<int64_t>(per_run, chunks) * kAccTokens);
+  const cudaError_t e = wide ? launch_finish<D, true>(p, (int)merge, (int)runs, run_tokens,
+                                                      (unsigned)grid, s)
+                             : launch_finish<D, false>(p, (int)merge, (int)runs, run_tokens,
+                                                       (unsigned)grid, s);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 template <bool FP8, int D, bool WEIGHTS = false, int NW = 4, int RING_KB = 64>
 pkv_status launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const DecodeParams &p,
                          cudaStream_t s) {
@@ -1491,21 +1588,16 @@ pkv_status launch_decode(const CUtensorMap &mk, const CUtensorMap &mv, const Dec
   if (launch_pdl(paged_decode_kernel<FP8, D, WEIGHTS, NW, RING_KB>, grid, dim3(C::NW * 32), C::SMEM_BYTES, s,
                  mk, mv, p) != cudaSuccess)
     return PKV_ERR_CUDA;
+  if constexpr (WEIGHTS) return launch_weights_finish<D>(p, s);
   if (p.max_parts > 1) {
     const long long rows = (long long)p.batch * p.num_heads;
     const cudaError_t e =
         p.max_parts > kMergeWarpMaxParts
-            ? launch_pdl(paged_decode_merge_wide_kernel<D, WEIGHTS>, dim3((unsigned)rows),
+            ? launch_pdl(paged_decode_merge_wide_kernel<D>, dim3((unsigned)rows),
                          dim3(kMergeWideThreads), 0, s, p)
-            : launch_pdl(paged_decode_merge_kernel<D, WEIGHTS>, dim3((unsigned)((rows + 7) / 8)),
+            : launch_pdl(paged_decode_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)),
                          dim3(256), 0, s, p);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
-  }
-  if constexpr (WEIGHTS) {
-    const dim3 acc((p.max_seq_len + kAccTokens - 1) / kAccTokens, p.num_kv_heads, p.batch);
-    if (acc.x > 0 && launch_pdl(weights_accumulate_kernel, acc, dim3(kAccThreads), 0, s, p) !=
-                         cudaSuccess)
-      return PKV_ERR_CUDA;
   }
   return PKV_OK;
 }
