@@ -162,7 +162,7 @@ def test_negative_weights(per_head):
 
 
 @pytest.mark.parametrize("L,keep", [(5000, 4999), (5000, 1), (20000, 7777), (70001, 2049),
-                                    (131072, 60000)])
+                                    (131072, 60000), (150001, 20000)])
 @pytest.mark.parametrize("per_head", [True, False])
 def test_long(L, keep, per_head):
     s = State([L, L // 3], 2, 64, "fp8_e4m3", seed=L, dst_lens=[keep, min(keep, L // 3)])
@@ -172,6 +172,14 @@ def test_long(L, keep, per_head):
 def test_long_in_place():
     s = State([30000, 9000], 2, 128, seed=8)
     s.run([12345, 8999], sink=4, recent=100)
+
+
+def test_more_keys_than_a_cluster_holds():
+    """150001 tokens: the keys past 8 x 16384 are read again in every round,
+    ties among them included."""
+    s = State([150001], 1, 64, "fp8_e4m3", seed=30, dst_lens=[70000])
+    s.w = (s.rng.integers(0, 9, s.w.shape) / 8.0).astype(np.float32)
+    s.run([70000], sink=1, recent=2, in_place=False)
 
 
 def test_clustered_weights():
