@@ -142,7 +142,8 @@ typedef struct {
  *                 NULL with num_heads 0 (k and v only).
  *   k, v          bf16 [num_tokens, num_kv_heads, head_dim], likewise.
  *   positions     int32 [num_axes, num_tokens], axes axis_stride elements
- *                 apart; any value, negative ones included.
+ *                 apart (0: one row serves every axis); any value, negative
+ *                 ones included.
  *   slot_mapping  as for paged_kv_write: a negative slot writes no k and v
  *                 (q is turned all the same); a slot past the pool is a
  *                 device range error (k and v of the token are skipped).
@@ -182,8 +183,9 @@ pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const void *k,
  *                 own, shared with no other sequence); otherwise int32
  *                 [batch, dst_max_blocks]: position i goes to row i % 16 of
  *                 block dst_tables[b][i / 16], and the blocks read stay as
- *                 they are.  No destination block may be read or written by
- *                 another sequence of the call.
+ *                 they are.  Unless dst_tables is block_tables itself (in
+ *                 place), no destination block may be among the blocks the
+ *                 call reads, nor belong to two sequences.
  *   dst_weights   NULL: weights move in place; otherwise fp32 [batch,
  *                 num_kv_heads, dst_weights_stride], not overlapping
  *                 weights.

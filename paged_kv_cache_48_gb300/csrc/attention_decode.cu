@@ -121,6 +121,9 @@ struct DecodeParams {
   long long weights_stride;
   int32_t logit_tokens;  // max_seq_len rounded up to whole blocks
   int32_t logit_heads;   // heads of a sub-group, rounded up to an even count
+  // 1: no sequence is split and a CTA holds all query heads of its kv head,
+  // so the decode kernel adds the weights itself and no second launch follows
+  int32_t weights_inline;
   float decay;
 };
 
@@ -219,6 +222,16 @@ struct Cfg {
 
 __device__ __forceinline__ int clamp_len(int L, int cap) {
   return L < 0 ? 0 : (L > cap ? cap : L);
+}
+
+// WEIGHTS: first position whose weight starts from 0, whatever its row holds:
+// the first one written by this call (L_in: the length as given).
+__device__ __forceinline__ int first_fresh(const DecodeParams &p, int b, int L_in, int L) {
+  if (p.k_new == nullptr || L_in != L || L == 0) return L;
+  if (!p.new_start_loc) return L - 1;
+  const int r0 = __ldg(p.new_start_loc + b), r1 = __ldg(p.new_start_loc + b + 1);
+  const bool ok = r1 >= r0 && r1 - r0 <= L && r0 >= 0 && r1 <= p.num_new;
+  return ok ? L - (r1 - r0) : L;
 }
 
 // Row of head_dim held by output fragment element (m-tile mt, upper half
@@ -1013,6 +1026,50 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
       if (d == 0) p.part_ml[slot] = make_float2(M, lsum);
     }
   }
+  if constexpr (WEIGHTS) {
+    if (p.weights_inline) {
+      // every warp's scores of this CTA's sequence are written (the barrier
+      // above); the heads' (M, 1 / l) from the warps' statistics
+      __shared__ float2 stat[8];
+      if (threadIdx.x < (unsigned)heads_here) {
+        const int h = threadIdx.x;
+        float M = -INFINITY, l = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          M = fmaxf(M, m_s[w][h]);
+          nan = nan || l_s[w][h] != l_s[w][h];
+        }
+        if (M != -INFINITY || nan) {
+#pragma unroll
+          for (int w = 0; w < C::NW; ++w)
+            if (m_s[w][h] != -INFINITY || l_s[w][h] != l_s[w][h])
+              l += exp2f(m_s[w][h] - M) * l_s[w][h];
+        }
+        stat[h] = l != 0.f ? make_float2(M, 1.f / l) : make_float2(0.f, 0.f);
+      }
+      __syncthreads();
+      const int fresh = first_fresh(p, b, len_ok ? L : -1, L);
+      float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
+      for (int t = threadIdx.x; t < L; t += C::NW * 32) {
+        const float old = (p.decay != 0.f && t < fresh) ? p.decay * w[t] : 0.f;
+        const float *row = lg_unit + (size_t)t * p.logit_heads;
+        float acc = 0.f;
+#pragma unroll
+        for (int hp = 0; hp < 4; ++hp) {
+          if (2 * hp >= heads_here) break;
+          const float2 s = __ldcs(reinterpret_cast<const float2 *>(row + 2 * hp));
+          const float2 a = stat[2 * hp];
+          if (a.y != 0.f) acc += exp2f(s.x - a.x) * a.y;
+          if (2 * hp + 1 < heads_here) {
+            const float2 c2 = stat[2 * hp + 1];
+            if (c2.y != 0.f) acc += exp2f(s.y - c2.x) * c2.y;
+          }
+        }
+        w[t] = old + acc;
+      }
+    }
+  }
   if (wait_at_exit) grid_dependency_wait();
 }
 
@@ -1275,18 +1332,7 @@ __device__ __forceinline__ void accumulate_weights(const DecodeParams &p, int b,
   if (t_begin >= L) return;
   t_end = min(t_end, L);
   const int nparts = L <= p.part_tokens ? 1 : (L + p.part_tokens - 1) / p.part_tokens;
-  // positions written by this call start from 0, whatever the row holds
-  int fresh = L;
-  if (p.k_new != nullptr && L_in == L) {
-    int n_new = 1;
-    bool ok = true;
-    if (p.new_start_loc) {
-      const int r0 = __ldg(p.new_start_loc + b), r1 = __ldg(p.new_start_loc + b + 1);
-      n_new = r1 - r0;
-      ok = n_new >= 0 && n_new <= L && r0 >= 0 && r1 <= p.num_new;
-    }
-    if (ok) fresh = L - n_new;
-  }
+  const int fresh = first_fresh(p, b, L_in, L);
   float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
   for (int h0 = 0; h0 < p.group; h0 += kAccHeads) {  // (one pass up to 128 heads a kv head)
     const int pass_heads = min(kAccHeads, p.group - h0);
@@ -1475,6 +1521,12 @@ std::atomic<int32_t> g_test_fail_seq{-1};
 // CTA each (paged_decode_merge_wide_kernel), fewer by one warp each.
 constexpr int kMergeWarpMaxParts = 8;
 
+// Up to this bound the decode kernel adds the weights itself
+// (DecodeParams::weights_inline): 4 sequences of 64 tokens 3.8 us against 5.5
+// with the second launch, 64 of 256 17.1 against 17.4; but 180 of 1000 tokens
+// 156 against 136, where a CTA's four warps alone would add up its tokens.
+constexpr int kInlineTokens = 256;
+
 // Partitions this short are owned by single warps (DecodeParams::warp_parts).
 constexpr int kWarpPartMaxTokens = 512;
 
@@ -1542,6 +1594,7 @@ cudaError_t launch_finish(const DecodeParams &p, int merge_ctas, int runs, int r
 template <int D>
 pkv_status launch_weights_finish(const DecodeParams &p, cudaStream_t s) {
   const int64_t rows = (int64_t)p.batch * p.num_heads;
+  if (p.weights_inline) return PKV_OK;
   const bool wide = p.max_parts > kMergeWarpMaxParts;
   const int64_t merge = p.max_parts > 1 ? (wide ? rows : (rows + 7) / 8) : 0;
   // runs of whole chunks, as long as still leaves eight CTAs an SM if every
@@ -1717,6 +1770,7 @@ pkv_status decode_entry(const void *q, const void *k_new, const void *v_new,
     p.weights = weights;
     p.weights_stride = weights_stride;
     p.decay = decay;
+    p.weights_inline = parts64 == 1 && group <= 8 && max_seq_len <= kInlineTokens;
   } else if (need > 0) {
     if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;

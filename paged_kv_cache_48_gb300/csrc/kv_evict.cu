@@ -11,7 +11,8 @@
 // describe only whole sequences leaving the cache (vLLM concept page,
 // compassingai.com, preemption); keeping part of one is this library's.
 //
-// Two launches.  evict_select_kernel: one cluster per choice finds the weight
+// Two launches (one where little is kept: evict_small_kernel).
+// evict_select_kernel: one cluster per choice finds the weight
 // of the last kept token by radix selection over order-preserving 32-bit
 // keys, then writes the kept positions in ascending order.  The second
 // launch moves the rows: evict_gather_kernel into other blocks, every row
@@ -80,6 +81,8 @@ __device__ __forceinline__ float rank_weight(const EvictParams &p, const float *
   return (float)s;
 }
 
+constexpr int kMaxCluster = 8;  // the portable size
+
 // Thread-block clusters (sm_90 and later): rank, size, barrier, and a load
 // from another CTA's shared memory.
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -115,7 +118,6 @@ __device__ __forceinline__ int load_cluster(const int *local, uint32_t rank) {
 // over twice as long).
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectMaxCluster = 8;  // the portable size
 // Keys a CTA holds (more are read again in every round): three CTAs fit an
 // SM with them, and 8 CTAs hold 131072.
 constexpr int kSelectMaxKeys = 16 * 1024;
@@ -125,19 +127,20 @@ __device__ __forceinline__ int warps_before(const int *v, int warp, int lane) {
   return __reduce_add_sync(0xffffffffu, lane < warp ? v[lane] : 0);
 }
 
+// Selects what choice (b, h) keeps, by the calling cluster of C CTAs (rank:
+// this CTA's), and writes its positions to kept[0 .. n-1].  Returns (n, L),
+// n < 0 where the sequence is left alone; the same in every thread.
+// launch_next: the following launch may start once every CTA is past its
+// passes over the keys.
 template <bool SUM>
-__global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
-    evict_select_kernel(const EvictParams p, int key_cap) {
-  extern __shared__ __align__(16) uint32_t keys[];
+__device__ __forceinline__ int2 select_kept(const EvictParams &p, int b, int h, int C, int rank,
+                                            uint32_t *keys, int key_cap, bool launch_next) {
   __shared__ int hist[4][256];
   __shared__ int totals[2];  // this CTA's keys above the last kept one's, and equal
   __shared__ int warp_a[kSelectWarps], warp_b[kSelectWarps];
   __shared__ int pick[2];  // digit, keys wanted within it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster_rank(), C = cluster_size();
-  const int h = blockIdx.x / C, b = blockIdx.y;
   for (int i = tid; i < 4 * 256; i += kSelectThreads) hist[i >> 8][i & 255] = 0;
-  grid_dependency_wait();
   int32_t *kept = p.kept + ((size_t)b * p.choices + h) * p.max_keep;
 
   const int L = __ldg(p.seq_lens + b), want = __ldg(p.keep + b);
@@ -145,21 +148,18 @@ __global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
   const bool bad = L < 0 || want < 0 || (long long)L > (long long)p.max_blocks * 16 ||
                    L > p.weights_stride || n > p.max_keep || n > p.dst_stride ||
                    (long long)n > (long long)p.dst_max_blocks * 16;
-  if (blockIdx.x == 0 && tid == 0) {
-    p.counts[b] = make_int2(bad ? -1 : n, L);
-    if (bad) record_error(&g_err_evict, PKV_ERR_RANGE, b);
-  }
-  if (bad) return;  // (the same in every CTA of the cluster, like the returns below)
+  if (bad && h == 0 && rank == 0 && tid == 0) record_error(&g_err_evict, PKV_ERR_RANGE, b);
+  if (bad) return make_int2(-1, L);  // (the same in every CTA, like the returns below)
   const int all = rank * kSelectThreads + tid, step = C * kSelectThreads;  // within the cluster
   const int recent = min(p.recent, n), sink = min(p.sink, n - recent);
   // the middle: tokens sink .. L - recent - 1, of which k are kept
   const int mid = L - recent - sink, k = n - recent - sink;
   for (int i = all; i < sink; i += step) kept[i] = i;
   for (int i = all; i < recent; i += step) kept[n - recent + i] = L - recent + i;
-  if (k == 0) return;
+  if (k == 0) return make_int2(n, L);
   if (k == mid) {
     for (int i = all; i < mid; i += step) kept[sink + i] = sink + i;
-    return;
+    return make_int2(n, L);
   }
 
   // this CTA's piece of the middle, in the head's weights or (SUM) the first
@@ -221,11 +221,11 @@ __global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
     if (tid < 256) {
       const int *own = &hist[round][255 - tid];
       if (C > 1) {
-        int part[kSelectMaxCluster];
+        int part[kMaxCluster];
 #pragma unroll
-        for (int r = 0; r < kSelectMaxCluster; ++r) part[r] = r < C ? load_cluster(own, r) : 0;
+        for (int r = 0; r < kMaxCluster; ++r) part[r] = r < C ? load_cluster(own, r) : 0;
 #pragma unroll
-        for (int r = 0; r < kSelectMaxCluster; ++r) c += part[r];
+        for (int r = 0; r < kMaxCluster; ++r) c += part[r];
       } else {
         c = *own;
       }
@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
     left = pick[1];
   }
 
-  // The moves may launch once every CTA is here (earlier, their waiting CTAs
-  // made the selection for eight rows of 131072 tokens 30 us slower).
-  allow_dependent_launch();
+  // (earlier, the waiting CTAs of the moves made the selection for eight rows
+  // of 131072 tokens 30 us slower)
+  if (launch_next) allow_dependent_launch();
   // Kept: every key above `prefix`, and the first `left` keys equal to it.
   // A warp owns a contiguous part of the piece: count, scan, write; a lane
   // takes four neighbouring keys at a time.
@@ -327,6 +327,18 @@ __global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
   }
   // no CTA leaves while another may still read its shared memory
   if (C > 1) cluster_sync();
+  return make_int2(n, L);
+}
+
+template <bool SUM>
+__global__ void __launch_bounds__(kSelectThreads, SUM ? 3 : 4)
+    evict_select_kernel(const EvictParams p, int key_cap) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  const int rank = cluster_rank(), C = cluster_size();
+  const int h = blockIdx.x / C, b = blockIdx.y;
+  grid_dependency_wait();
+  const int2 c = select_kept<SUM>(p, b, h, C, rank, keys, key_cap, true);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.counts[b] = c;
 }
 
 // Row index (head rows of the pool) of position t through a table row; -1
@@ -415,31 +427,48 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
   }
 }
 
-// In place: token kept[i] moves to position i <= kept[i].  One CTA takes one
-// plane (K, V or the weights) of one (sequence, kv head) and walks it in
-// chunks in ascending order: a chunk is read whole before it is written, and
-// every later chunk's sources lie at or above its own positions, past all
-// positions written so far.
+// In place: token kept[i] moves to position i <= kept[i].  A cluster of C
+// CTAs takes one plane (K, V or the weights) of one (sequence, kv head) and
+// walks it in chunks in ascending order, a C-th of each chunk a CTA.  A chunk
+// is read whole, by every CTA, before any of it is written, and every later
+// chunk's sources lie at or above its own positions, past all positions
+// written so far; so (AHEAD) the next chunk's rows may be on their way when a
+// chunk is written, and the rows after that be looked up meanwhile.  With
+// many planes the other CTAs of an SM hide a chunk's latency and the registers
+// of a chunk in flight cost more than they give (64 sequences of 8 heads: 91
+// us, 99 with AHEAD); with few, the latency of a chunk bounds it, hence the
+// clusters (28000 of 32768 tokens of one sequence of 8 heads: 383 us with a
+// CTA a plane, 139 with 8 and PER = 4, 101 with PER = 8; eight long sequences:
+// 369, 284 and 316).
 constexpr int kCompactThreads = 256;
-constexpr int kCompactTokens = 128;
+constexpr int kCompactWeights = 8;  // weights of a thread in a chunk
 
 template <int RB>
+constexpr int compact_tokens(int per) {  // of a CTA in a chunk
+  return kCompactThreads * per / (RB / 16);
+}
+
+// PER: 16-byte vectors of a thread in a chunk.
+template <int RB, int PER, bool AHEAD>
 __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const EvictParams p) {
   constexpr int LANES = RB / 16;
-  constexpr int PER = kCompactTokens * LANES / kCompactThreads;  // vectors of a thread
-  __shared__ long long from_s[2][kCompactTokens], to_s[2][kCompactTokens];
+  constexpr int TOKENS = compact_tokens<RB>(PER);
+  __shared__ long long from_s[3][TOKENS], to_s[3][TOKENS];  // row indices, -1: nothing to move
   grid_dependency_wait();
   allow_dependent_launch();
-  const int b = blockIdx.z, h = blockIdx.y, plane = blockIdx.x;
+  const int C = cluster_size(), rank = cluster_rank();
+  const int b = blockIdx.z, h = blockIdx.y, plane = blockIdx.x / C;
   const int tid = threadIdx.x;
   const int2 c = p.counts[b];
   const int n = c.x, L = c.y;
-  if (plane == 0 && h == 0 && tid == 0) p.new_seq_lens[b] = n < 0 ? L : n;
+  if (blockIdx.x == 0 && h == 0 && tid == 0) p.new_seq_lens[b] = n < 0 ? L : n;
   const bool moves = p.dst_tables == p.tables;  // K and V in place
-  if (moves) finish_row(p, b, h, c, plane * kCompactThreads + tid, 3 * kCompactThreads);
+  if (moves)
+    finish_row(p, b, h, c, blockIdx.x * kCompactThreads + tid, gridDim.x * kCompactThreads);
   if (n < 0) return;  // left alone
   const int32_t *kept = p.kept + ((size_t)b * p.choices + (p.choices > 1 ? h : 0)) * p.max_keep;
   if (plane == 2) {
+    if (rank > 0) return;
     const size_t bh = (size_t)b * p.num_kv_heads + h;
     float *w = p.dst_weights + bh * p.dst_stride;
     if (!p.weights_in_place) {  // (into other blocks: moved with the rows)
@@ -449,11 +478,19 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Ev
       return;
     }
     if (n == L) return;  // nothing given up
-    for (int i0 = 0; i0 < n; i0 += kCompactThreads) {
-      const int i = i0 + tid;
-      const float x = i < n ? w[kept[i]] : 0.f;
+    for (int i0 = tid; i0 - tid < n; i0 += kCompactThreads * kCompactWeights) {
+      float x[kCompactWeights];
+#pragma unroll
+      for (int k = 0; k < kCompactWeights; ++k) {
+        const int i = i0 + k * kCompactThreads;
+        if (i < n) x[k] = w[kept[i]];
+      }
       __syncthreads();
-      if (i < n) w[i] = x;
+#pragma unroll
+      for (int k = 0; k < kCompactWeights; ++k) {
+        const int i = i0 + k * kCompactThreads;
+        if (i < n) w[i] = x[k];
+      }
     }
     __syncthreads();
     for (int t = n + tid; t < L; t += kCompactThreads) w[t] = 0.f;
@@ -461,35 +498,123 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(const Ev
   }
   if (!moves || n == L) return;
   uint4 *pool = reinterpret_cast<uint4 *>(plane == 0 ? p.k_cache : p.v_cache);
-  for (int i0 = 0; i0 < n; i0 += kCompactTokens) {
-    const int buf = (i0 / kCompactTokens) & 1;
-    if (tid < kCompactTokens) {
+  const int chunks = (n + C * TOKENS - 1) / (C * TOKENS);
+  auto look_up = [&](int chunk) {  // this CTA's rows of a chunk
+    const long long base = ((long long)chunk * C + rank) * TOKENS;
+    for (int k = tid; k < TOKENS; k += kCompactThreads) {
       long long from = -1, to = -1;
-      if (i0 + tid < n) {
-        const int t = kept[i0 + tid];
-        if (t != i0 + tid) {  // (a token that stays needs no copy)
+      if (base + k < n) {
+        const int i = (int)base + k, t = kept[i];
+        if (t != i) {  // (a token that stays needs no copy)
           from = row_of(p, p.tables, p.max_blocks, b, h, t);
-          to = row_of(p, p.tables, p.max_blocks, b, h, i0 + tid);
+          to = row_of(p, p.tables, p.max_blocks, b, h, i);
           if (from < 0 || to < 0) from = to = -1;
         }
       }
-      from_s[buf][tid] = from;
-      to_s[buf][tid] = to;
+      from_s[chunk % 3][k] = from;
+      to_s[chunk % 3][k] = to;
     }
-    __syncthreads();
-    uint4 x[PER];
+  };
+  uint4 next[PER];
+  auto read = [&](int chunk) {
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int idx = k * kCompactThreads + tid;
-      const long long from = from_s[buf][idx / LANES];
-      if (from >= 0) x[k] = pool[from * LANES + idx % LANES];
+      const long long from = from_s[chunk % 3][idx / LANES];
+      if (from >= 0) next[k] = pool[from * LANES + idx % LANES];
     }
+  };
+  if (AHEAD) {
+    look_up(0);
     __syncthreads();
+    read(0);
+    look_up(1);
+  }
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    if (!AHEAD) look_up(chunk);
+    __syncthreads();  // rows looked up: of this chunk, or (AHEAD) the next
+    if (!AHEAD) read(chunk);
+    uint4 now[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) now[k] = next[k];
+    if (AHEAD && chunk + 1 < chunks) {
+      read(chunk + 1);
+      look_up(chunk + 2);
+    }
+    // every CTA of the cluster has read this chunk
+    if (C > 1)
+      cluster_sync();
+    else
+      __syncthreads();
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int idx = k * kCompactThreads + tid;
-      const long long to = to_s[buf][idx / LANES];
-      if (to >= 0) pool[to * LANES + idx % LANES] = x[k];
+      const long long to = to_s[chunk % 3][idx / LANES];
+      if (to >= 0) pool[to * LANES + idx % LANES] = now[k];
+    }
+  }
+}
+
+// Few tokens kept by few rows: selection and moves in one launch.  The CTA
+// that chose for a head moves the head's tokens: all rows of a plane are read
+// before one is written, which serves moves in place and into other blocks
+// alike.  4 sequences of 8 heads of 100 tokens 6.3 us against 7.8 in two
+// launches, 16 of 1024 tokens 9.8 against 12.8; but 64 of 1024 36 against 33,
+// and a choice for 8 heads moved by its one CTA 41 against 12.
+constexpr int kSmallKeep = 256;  // tokens kept by a sequence at most
+constexpr int kSmallRow = 4096;  // keys of a row at most
+
+template <int RB>
+__global__ void __launch_bounds__(kSelectThreads)
+    evict_small_kernel(const EvictParams p, int key_cap) {
+  constexpr int LANES = RB / 16;
+  constexpr int PER = kSmallKeep * LANES / kSelectThreads;  // vectors of a thread in a plane
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ long long from_s[kSmallKeep], to_s[kSmallKeep];
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int2 c = select_kept<false>(p, b, h, 1, 0, keys, key_cap, false);
+  const int n = c.x, L = c.y;
+  if (h == 0 && tid == 0) p.new_seq_lens[b] = n < 0 ? L : n;
+  __syncthreads();  // kept is written
+  finish_row(p, b, h, c, tid, kSelectThreads);
+  if (n < 0) return;
+  const int32_t *kept = p.kept + ((size_t)b * p.choices + h) * p.max_keep;
+  const bool in_place = p.dst_tables == p.tables;
+  const size_t bh = (size_t)b * p.num_kv_heads + h;
+  float x = 0.f;
+  if (tid < n) {
+    const int t = kept[tid];
+    x = p.weights[bh * p.weights_stride + t];
+    long long from = -1, to = -1;
+    if (!in_place || t != tid) {
+      from = row_of(p, p.tables, p.max_blocks, b, h, t);
+      to = row_of(p, p.dst_tables, p.dst_max_blocks, b, h, tid);
+      if (from < 0 || to < 0) from = to = -1;
+    }
+    from_s[tid] = from;
+    to_s[tid] = to;
+  }
+  __syncthreads();  // weights read, rows looked up
+  float *w = p.dst_weights + bh * p.dst_stride;
+  if (tid < n) w[tid] = x;
+  if (p.weights_in_place)  // (other weights: finish_row)
+    for (int t = n + tid; t < L; t += kSelectThreads) w[t] = 0.f;
+#pragma unroll
+  for (int plane = 0; plane < 2; ++plane) {
+    uint4 *pool = reinterpret_cast<uint4 *>(plane == 0 ? p.k_cache : p.v_cache);
+    uint4 v[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = (k * kSelectThreads + tid) / LANES, u = tid % LANES;
+      if (i < n && from_s[i] >= 0) v[k] = pool[from_s[i] * LANES + u];
+    }
+    __syncthreads();  // the plane is read
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = (k * kSelectThreads + tid) / LANES, u = tid % LANES;
+      if (i < n && to_s[i] >= 0) pool[to_s[i] * LANES + u] = v[k];
     }
   }
 }
@@ -513,39 +638,31 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// The selection: a cluster per choice, of as many CTAs as hold a row's keys,
-// or more of them (at least 1024 keys each) while all fit the GPU at once.
-template <bool SUM>
-cudaError_t launch_select(const EvictParams &p, cudaStream_t s) {
-  const int64_t longest = std::min<int64_t>(p.weights_stride, (int64_t)p.max_blocks * 16);
-  const int64_t rows = (int64_t)p.choices * p.batch, slots = 3 * (int64_t)device_sm_count();
-  int C = 1;
-  while (C < kSelectMaxCluster &&
-         (longest > (int64_t)C * kSelectMaxKeys ||
-          (rows * C * 2 <= slots && longest >= (int64_t)C * 2048)))
-    C *= 2;
-  const int64_t piece = ((longest + C - 1) / C + 31) / 32 * 32;
-  const int cap = (int)std::min<int64_t>(std::max<int64_t>(piece, 32), kSelectMaxKeys);
+// Lets a selection kernel hold its keys, once per device.
+template <auto Kernel>
+cudaError_t allow_keys() {
   static int configured[64] = {0};
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!configured[dev]) {
-      e = cudaFuncSetAttribute(evict_select_kernel<SUM>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSelectMaxKeys * (int)sizeof(uint32_t));
-      if (e != cudaSuccess) return e;
-      configured[dev] = 1;
-    }
-  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (configured[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSelectMaxKeys * (int)sizeof(uint32_t));
+  if (e == cudaSuccess) configured[dev] = 1;
+  return e;
+}
+
+// A launch in clusters of C CTAs along x, with programmatic serialisation.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int C,
+                            cudaStream_t s, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.choices * C, p.batch);
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = cap * sizeof(uint32_t);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -555,7 +672,48 @@ cudaError_t launch_select(const EvictParams &p, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<SUM>, p, cap);
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+int64_t longest_row(const EvictParams &p) {
+  return std::min<int64_t>(p.weights_stride, (int64_t)p.max_blocks * 16);
+}
+
+// The selection: a cluster per choice, of as many CTAs as hold a row's keys,
+// or more of them (at least 1024 keys each) while all fit the GPU at once.
+template <bool SUM>
+cudaError_t launch_select(const EvictParams &p, cudaStream_t s) {
+  const cudaError_t e = allow_keys<evict_select_kernel<SUM>>();
+  if (e != cudaSuccess) return e;
+  const int64_t longest = longest_row(p);
+  const int64_t rows = (int64_t)p.choices * p.batch, slots = 3 * (int64_t)device_sm_count();
+  int C = 1;
+  while (C < kMaxCluster &&
+         (longest > (int64_t)C * kSelectMaxKeys ||
+          (rows * C * 2 <= slots && longest >= (int64_t)C * 2048)))
+    C *= 2;
+  const int64_t piece = ((longest + C - 1) / C + 31) / 32 * 32;
+  const int cap = (int)std::min<int64_t>(std::max<int64_t>(piece, 32), kSelectMaxKeys);
+  return launch_clusters(evict_select_kernel<SUM>, dim3(p.choices * C, p.batch), kSelectThreads,
+                         cap * sizeof(uint32_t), C, s, p, cap);
+}
+
+// One launch for everything (see evict_small_kernel) where a CTA holds a row's
+// keys and its moves are few.  new_seq_lens must not be seq_lens then: other
+// CTAs of the sequence may still read the old length.
+bool one_launch(const EvictParams &p) {
+  return p.max_keep <= kSmallKeep && longest_row(p) <= kSmallRow &&
+         p.choices == p.num_kv_heads &&
+         (int64_t)p.choices * p.batch <= device_sm_count() && p.new_seq_lens != p.seq_lens;
+}
+
+template <int RB>
+cudaError_t launch_small(const EvictParams &p, cudaStream_t s) {
+  const cudaError_t e = allow_keys<evict_small_kernel<RB>>();
+  if (e != cudaSuccess) return e;
+  const int cap = (int)((std::max<int64_t>(longest_row(p), 1) + 31) / 32 * 32);
+  return launch_clusters(evict_small_kernel<RB>, dim3(p.choices, p.batch), kSelectThreads,
+                         cap * sizeof(uint32_t), 1, s, p, cap);
 }
 
 template <int RB>
@@ -567,9 +725,20 @@ cudaError_t launch_move(const EvictParams &p, cudaStream_t s) {
     e = launch_pdl(evict_gather_kernel<RB>,
                    dim3(std::max(1, (p.max_keep + per - 1) / per), p.num_kv_heads, p.batch),
                    dim3(kGatherThreads), s, p);
-  if (e == cudaSuccess && (in_place || p.weights_in_place))
-    e = launch_pdl(evict_compact_kernel<RB>, dim3(3, p.num_kv_heads, p.batch),
-                   dim3(kCompactThreads), s, p);
+  if (e == cudaSuccess && (in_place || p.weights_in_place)) {
+    // K, V and weights planes; with few of them, clusters of CTAs for each,
+    // and where even those leave SMs over, longer chunks
+    const int64_t planes = 2 * (int64_t)p.num_kv_heads * p.batch, sms = device_sm_count();
+    const bool few = planes * kMaxCluster <= sms;
+    int C = 1;
+    while (in_place && C < kMaxCluster && planes * C * 2 <= 4 * sms &&
+           p.max_keep > (int64_t)C * compact_tokens<RB>(few ? 8 : 4))
+      C *= 2;
+    auto kernel = C == 1 ? evict_compact_kernel<RB, 8, false>
+                  : few  ? evict_compact_kernel<RB, 8, true>
+                         : evict_compact_kernel<RB, 4, true>;
+    e = launch_clusters(kernel, dim3(3 * C, p.num_kv_heads, p.batch), kCompactThreads, 0, C, s, p);
+  }
   return e;
 }
 
@@ -654,11 +823,18 @@ extern "C" pkv_status paged_kv_evict(const pkv_cache *cache, const int32_t *bloc
   p.recent = recent;
   p.row_bytes = cache->head_dim * (cache->dtype == PKV_FP8_E4M3 ? 1 : 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (one_launch(p)) {
+    e = p.row_bytes == 256   ? launch_small<256>(p, s)
+        : p.row_bytes == 128 ? launch_small<128>(p, s)
+                             : launch_small<64>(p, s);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   const bool sum = p.choices < p.num_kv_heads;  // one choice by the heads' sum
-  if ((sum ? launch_select<true>(p, s) : launch_select<false>(p, s)) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  const cudaError_t e = p.row_bytes == 256   ? launch_move<256>(p, s)
-                        : p.row_bytes == 128 ? launch_move<128>(p, s)
-                                             : launch_move<64>(p, s);
+  e = sum ? launch_select<true>(p, s) : launch_select<false>(p, s);
+  if (e == cudaSuccess)
+    e = p.row_bytes == 256   ? launch_move<256>(p, s)
+        : p.row_bytes == 128 ? launch_move<128>(p, s)
+                             : launch_move<64>(p, s);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

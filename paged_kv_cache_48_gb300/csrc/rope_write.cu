@@ -287,7 +287,7 @@ extern "C" pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const
       k_stride > kMaxStride || v_stride > kMaxStride ||
       (num_heads > 0 && (q_stride > kMaxStride || q_out_stride > kMaxStride)))
     return PKV_ERR_ARG;
-  if (k_stride < kv_len || v_stride < kv_len || axis_stride < num_tokens ||
+  if (k_stride < kv_len || v_stride < kv_len || axis_stride < 0 ||
       (num_heads > 0 && (q_stride < q_len || q_out_stride < q_len)))
     return PKV_ERR_ARG;
   if ((k_stride | v_stride | (num_heads > 0 ? q_stride | q_out_stride : 0)) & 7)

@@ -89,6 +89,8 @@ CASES = {
                                     seq_lens=[0, 1, 16, 17, 1025]), 0),
     "g11_split": (lambda: wl.make_workload("g11", 2, 22, 2, 128, 0, 0, 33,
                                            seq_lens=[2100, 3]), 1024),
+    "unsplit": (lambda: wl.make_workload("unsplit", 3, 8, 2, 128, 0, 0, 36,
+                                         seq_lens=[700, 256, 257]), 704),
     "g136": (lambda: wl.make_workload("g136", 2, 136, 1, 64, 0, 0, 35, seq_lens=[37, 130]), 0),
     "one_long": (lambda: wl.make_workload("one", 1, 8, 1, 128, 0, 0, 34, seq_lens=[6001]), 0),
 }

@@ -111,35 +111,44 @@ LENS = [0, 1, 15, 16, 17, 100, 333, 64]
 KEEP = [5, 1, 16, 9, 17, 33, 100, 0]
 
 
+# new_seq_lens being seq_lens takes the two-launch form at every size; with
+# few tokens kept and lengths of their own, one launch does it all.
+ALIAS = pytest.mark.parametrize("alias", [False, True], ids=["one_launch", "two_launches"])
+
+
+@ALIAS
 @pytest.mark.parametrize("per_head", [True, False])
 @pytest.mark.parametrize("kv_dtype,D", [("bf16", 64), ("bf16", 128), ("fp8_e4m3", 64),
                                         ("fp8_e4m3", 128)])
 @pytest.mark.parametrize("in_place", [True, False])
-def test_ragged(in_place, kv_dtype, D, per_head):
+def test_ragged(in_place, kv_dtype, D, per_head, alias):
     n = np.minimum(LENS, KEEP)
     s = State(LENS, 3, D, kv_dtype, seed=D, dst_lens=None if in_place else n)
-    s.run(KEEP, sink=2, recent=5, per_head=per_head, in_place=in_place)
+    s.run(KEEP, sink=2, recent=5, per_head=per_head, in_place=in_place, alias=alias)
 
 
+@ALIAS
 @pytest.mark.parametrize("sink,recent", [(0, 0), (1000, 0), (0, 1000), (20, 30), (3, 47), (50, 50)])
-def test_protected_tokens(sink, recent):
+def test_protected_tokens(sink, recent, alias):
     s = State([50, 200, 51, 49], seed=sink + recent)
-    s.run([50, 50, 50, 50], sink=sink, recent=recent)
+    s.run([50, 50, 50, 50], sink=sink, recent=recent, alias=alias)
 
 
+@ALIAS
 @pytest.mark.parametrize("in_place", [True, False])
-def test_separate_weights(in_place):
+def test_separate_weights(in_place, alias):
     lens, keep = [90, 20, 300, 7], [40, 30, 123, 7]
     s = State(lens, seed=3, dst_lens=None if in_place else np.minimum(lens, keep))
     g = np.random.default_rng(1).random((4, 2, 130)).astype(np.float32)  # narrower than weights
-    s.run(keep, sink=1, recent=2, in_place=in_place, dst_w=g)
+    s.run(keep, sink=1, recent=2, in_place=in_place, dst_w=g, alias=alias)
     s = State(lens, seed=3, dst_lens=None if in_place else np.minimum(lens, keep))
     g = np.random.default_rng(1).random((4, 2, 500)).astype(np.float32)  # wider
-    s.run(keep, sink=1, recent=2, in_place=in_place, dst_w=g)
+    s.run(keep, sink=1, recent=2, in_place=in_place, dst_w=g, alias=alias)
 
 
+@ALIAS
 @pytest.mark.parametrize("per_head", [True, False])
-def test_ties_zeros_and_special_values(per_head):
+def test_ties_zeros_and_special_values(per_head, alias):
     """Equal weights go by position; NaN below -inf below all; -0 ties 0;
     subnormals are ordered."""
     s = State([400, 400, 400, 400, 64], 4, seed=5)
@@ -151,7 +160,7 @@ def test_ties_zeros_and_special_values(per_head):
     s.w[2, :, 4::9] = -np.inf
     s.w[3] = s.rng.integers(0, 6, s.w[3].shape).astype(np.float32)
     s.w[4, :, :64] = (s.rng.integers(0, 4, (4, 64)) * 2.0 ** -149).astype(np.float32)
-    s.run([100, 101, 250, 77, 20], sink=4, recent=9, per_head=per_head)
+    s.run([100, 101, 250, 77, 20], sink=4, recent=9, per_head=per_head, alias=alias)
 
 
 @pytest.mark.parametrize("per_head", [True, False])
@@ -167,6 +176,30 @@ def test_negative_weights(per_head):
 def test_long(L, keep, per_head):
     s = State([L, L // 3], 2, 64, "fp8_e4m3", seed=L, dst_lens=[keep, min(keep, L // 3)])
     s.run([keep, keep], sink=4, recent=min(64, keep // 2), per_head=per_head, in_place=False)
+
+
+@pytest.mark.parametrize("kv_dtype,D", [("bf16", 128), ("fp8_e4m3", 64)])
+@pytest.mark.parametrize("B,Hkv", [(6, 4), (2, 3)])
+def test_in_place_by_clusters(B, Hkv, kv_dtype, D):
+    """Planes walked by clusters of CTAs: few of them, and a middle count;
+    chunks where nothing, something and everything moves."""
+    lens = [5000 - 311 * b for b in range(B)]
+    s = State(lens, Hkv, D, kv_dtype, seed=B)
+    s.w[0, :, :1500] += 1e6  # a long run that stays where it is
+    s.run([4000 - 500 * b for b in range(B)], sink=1, recent=7)
+
+
+@pytest.mark.parametrize("Hkv", [8, 9])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_borders_of_the_one_launch_form(in_place, Hkv):
+    """256 and 257 tokens kept, rows of 4096 and 4097 keys, one choice for all
+    heads: either side of the rule gives the same."""
+    for L, keep in ((4096, 256), (4097, 256), (1000, 257), (256, 256), (257, 255)):
+        n = [keep, min(keep, 300)]
+        s = State([L, 300], Hkv, 64, seed=L + keep, dst_lens=None if in_place else n)
+        s.run(n, sink=3, recent=11, per_head=Hkv == 8, in_place=in_place)
+    s = State([4096, 300], 2, 128, seed=31, dst_lens=None if in_place else [256, 256])
+    s.run([256, 256], sink=3, recent=11, in_place=in_place)
 
 
 def test_long_in_place():
@@ -210,37 +243,39 @@ def test_max_keep_above_and_kept_zero():
     s.run([0, 0], max_keep=0)
 
 
-def test_range_errors_leave_the_sequence_alone():
+@ALIAS
+def test_range_errors_leave_the_sequence_alone(alias):
     lens = [40, 60, 50, 30, 20]
     s = State(lens, seed=14)
-    s.run([10, -1, 20, 30, 20], bad=(1,), status=5)                 # negative keep
+    s.run([10, -1, 20, 30, 20], bad=(1,), status=5, alias=alias)    # negative keep
     s = State(lens, seed=15)
-    s.run([10, 45, 20, 30, 20], max_keep=40, bad=(1,), status=5)    # n past max_keep
+    s.run([10, 45, 20, 30, 20], max_keep=40, bad=(1,), status=5, alias=alias)    # n past max_keep
     s = State(lens, seed=16, width=55)                              # past the weights row
-    s.run([10, 20, 20, 30, 20], bad=(1,), status=5)
+    s.run([10, 20, 20, 30, 20], bad=(1,), status=5, alias=alias)
     s = State(lens, seed=17)
     s.lens[2] = -3
-    s.run([10, 20, 20, 30, 20], bad=(2,), status=5)
+    s.run([10, 20, 20, 30, 20], bad=(2,), status=5, alias=alias)
     s = State(lens, seed=18)
     s.lens[0] = 16 * s.tables.shape[1] + 1                          # past the table
     s.w = np.pad(s.w, ((0, 0), (0, 0), (0, 20)))
     s.S = s.w.shape[2]
-    s.run([10, 20, 20, 30, 20], bad=(0,), status=5)
+    s.run([10, 20, 20, 30, 20], bad=(0,), status=5, alias=alias)
     s = State([40, 60], seed=19, dst_lens=[16, 16])                 # past dst_tables
-    s.run([10, 17], in_place=False, bad=(1,), status=5)
+    s.run([10, 17], in_place=False, bad=(1,), status=5, alias=alias)
     s = State([40, 60], seed=20)                                    # past dst_weights
-    s.run([10, 17], dst_w=np.ones((2, 2, 16), np.float32), bad=(1,), status=5)
+    s.run([10, 17], dst_w=np.ones((2, 2, 16), np.float32), bad=(1,), status=5, alias=alias)
 
 
-def test_bad_blocks_are_skipped():
+@ALIAS
+def test_bad_blocks_are_skipped(alias):
     s = State([100, 80], seed=21)
     s.tables[0, 3] = 10 ** 6
     s.tables[1, 0] = -1
-    s.run([40, 30], recent=20, status=5)
+    s.run([40, 30], recent=20, status=5, alias=alias)
     s = State([100, 80], seed=22, dst_lens=[40, 30])
     s.tables[0, 6] = -5
     s.dst[1, 1] = 10 ** 6
-    s.run([40, 30], recent=20, in_place=False, status=5)
+    s.run([40, 30], recent=20, in_place=False, status=5, alias=alias)
 
 
 def test_deterministic():

@@ -185,6 +185,16 @@ def test_in_place_and_slices(T):
     _check(q, k, v, q, cache, slots, pos, rope, q_in=q_in)
 
 
+def test_one_row_of_positions_for_every_axis():
+    """Text only: positions expanded over the axes (stride 0)."""
+    T = 19
+    rng, q, k, v, cache, slots = _make(T, 4, 2, 64, seed=14)
+    rope = RotaryAxes(64, [12, 10, 10])
+    pos = torch.from_numpy(rng.integers(0, 9999, T).astype(np.int32)).cuda()
+    qo = paged_kv_rope_write(q, k, v, pos.expand(3, T), slots, cache, rope)
+    _check(q, k, v, qo, cache, slots, torch.stack([pos, pos, pos]), rope)
+
+
 @pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
 def test_padding_and_bad_slots(kv_dtype):
     T = 21

@@ -49,7 +49,7 @@ def _rope_call(lib, q=1 << 20, qs=256, k=1 << 21, ks=256, v=1 << 22, vs=256, pos
     (dict(ks=248), ARG),                   # shorter than a row
     (dict(qs=260), ARG),                   # not a multiple of 8
     (dict(os=248), ARG),
-    (dict(axs=9), ARG),                    # axes overlap
+    (dict(axs=-1), ARG),
     (dict(T=1 << 31), ARG),
     (dict(ks=1 << 31), ARG),
     (dict(out=(1 << 20) + 16), ARG),       # q_out shifted over q
