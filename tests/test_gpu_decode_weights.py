@@ -9,7 +9,7 @@ import torch
 import harness
 import lifetime_ref as ref
 from paged_kv_cache_48_gb300 import _native
-from paged_kv_cache_48_gb300 import (PagedKVError, paged_attention_decode,
+from paged_kv_cache_48_gb300 import (PagedKVCache, PagedKVError, paged_attention_decode,
                                      paged_attention_decode_step,
                                      paged_attention_decode_weights,
                                      paged_attention_decode_weights_workspace_bytes,
@@ -354,3 +354,132 @@ def test_binding_refusals():
     bad(PagedKVError, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     bad(PagedKVError, decay=float("nan"))
     assert bool((w == 0).all())
+
+
+def _many(B, Hq, Hkv, D, lens, kv_dtype="bf16", seed=0):
+    """Inputs of a large batch, made on the GPU: (cache, q, tables, lens)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    nb = [(int(n) + 15) // 16 for n in lens]
+    total = sum(nb) + 3
+    shape = (total, 16, Hkv, D)
+    x = [torch.empty(shape, device="cuda").normal_(generator=g) for _ in range(2)]
+    if kv_dtype == "bf16":
+        cache = PagedKVCache(x[0].bfloat16(), x[1].bfloat16())
+    else:
+        s = 8.0 / 448
+        c = [(v / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) for v in x]
+        cache = PagedKVCache(c[0], c[1], kv_dtype, s, s)
+    order = torch.randperm(total, generator=g, device="cuda").to(torch.int32).cpu().numpy()
+    tables = np.full((B, max(1, max(nb))), -1, np.int32)
+    at = 0
+    for b, n in enumerate(nb):
+        tables[b, :n] = order[at:at + n]
+        at += n
+    q = torch.empty(B, Hq, D, device="cuda").normal_(generator=g).bfloat16()
+    return cache, q, tables, np.asarray(lens, np.int32)
+
+
+def _exact_weights(cache, q, tables, lens, scale):
+    """(summed weights [B, Hkv, S] float64, relative tolerance), on the GPU."""
+    B, Hq, D = q.shape
+    Hkv, S = cache.num_kv_heads, int(max(lens))
+    kc = cache.key_cache.double() if cache.kv_dtype == "bf16" else \
+        cache.key_cache.view(torch.float8_e4m3fn).double() * float(np.float32(cache.k_scale))
+    w = torch.zeros(B, Hkv, S, dtype=torch.float64, device="cuda")
+    bound = 0.0
+    for b, L in enumerate(lens):
+        L = int(L)
+        if L == 0:
+            continue
+        t = torch.from_numpy(tables[b, :(L + 15) // 16].astype(np.int64)).cuda()
+        k = kc[t].flatten(0, 1)[:L]
+        for h in range(Hkv):
+            qh = q[b, h * (Hq // Hkv):(h + 1) * (Hq // Hkv)].double()
+            w[b, h, :L] = torch.softmax(scale * qh @ k[:, h].t(), -1).sum(0)
+            bound = max(bound, float((scale * qh.abs() @ k[:, h].abs().t()).max()))
+    return w, ref.weights_tolerance(D, int(max(lens)), Hq // Hkv, bound)
+
+
+LARGE = {
+    # batch, q heads, kv heads, head_dim, longest, partition, cache
+    "g4": (80, 32, 8, 128, 2500, 1024, "bf16"),
+    "g8_ragged": (70, 64, 8, 64, 2000, 528, "bf16"),
+    "g5_fp8": (90, 40, 8, 64, 1800, 640, "fp8_e4m3"),
+    "g1_auto": (130, 8, 8, 64, 2100, 0, "bf16"),
+    "g2_two_heads": (300, 4, 2, 64, 1700, 544, "bf16"),
+}
+
+
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_batches(name):
+    """Many waves of CTAs, several partitions a sequence, runs of several
+    chunks: every token's weight is right, none is added twice or left out,
+    whatever the workspace held, and calls repeat to the bit."""
+    B, Hq, Hkv, D, longest, pt, kv_dtype = LARGE[name]
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, longest + 1, B)
+    lens[0], lens[3], lens[-1] = 0, longest, longest
+    cache, q, tables, lens = _many(B, Hq, Hkv, D, lens, kv_dtype)
+    gt, gl = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+    scale = D ** -0.5
+    w64, tol = _exact_weights(cache, q, tables, lens, scale)
+    S = longest + 7
+    need = paged_attention_decode_weights_workspace_bytes(B, Hq, Hkv, D, longest, pt)
+    plain = paged_attention_decode(q, cache, gt, gl, scale, longest, partition_tokens=pt)
+    first = None
+    for fill in (0, 0xFF, 0x5A, None, None):
+        if fill is not None:
+            ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        w = torch.ones(B, Hkv, S, device="cuda")
+        out = paged_attention_decode_weights(q, cache, gt, gl, scale, longest, w, decay=0.5,
+                                             partition_tokens=pt, workspace=ws)
+        assert pkv_check()[0] == 0
+        assert torch.equal(out.view(torch.int16), plain.view(torch.int16))
+        if first is None:
+            first = w
+            t = torch.arange(S, device="cuda")
+            valid = (t < gl[:, None])[:, None].expand_as(w)
+            assert bool((w[~valid] == 1.0).all())
+            got = w[:, :, :w64.shape[2]].double()
+            want = torch.where(valid[:, :, :w64.shape[2]], w64 + 0.5, 1.0)
+            lim = tol * w64 + 2.0 ** -23 * want
+            assert bool(((got - want).abs() <= lim).all())
+        assert torch.equal(w, first)
+
+
+def test_replayed_with_other_queries_and_lengths():
+    """One graph replayed with other queries and lengths in its inputs: nothing
+    of an earlier replay is left in the result."""
+    B, Hq, Hkv, D, longest, pt = 80, 32, 8, 64, 2200, 1024
+    rng = np.random.default_rng(77)
+    cache, q, tables, lens = _many(B, Hq, Hkv, D, np.full(B, longest), seed=5)
+    gt = torch.from_numpy(tables).cuda()
+    gl = torch.from_numpy(lens).cuda()
+    need = paged_attention_decode_weights_workspace_bytes(B, Hq, Hkv, D, longest, pt)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    w, out = torch.zeros(B, Hkv, longest, device="cuda"), torch.empty_like(q)
+
+    def step():
+        paged_attention_decode_weights(q, cache, gt, gl, 0.125, longest, w, decay=0.0, out=out,
+                                       partition_tokens=pt, workspace=ws)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        q.normal_()
+        new = rng.integers(1, longest + 1, B).astype(np.int32)
+        gl.copy_(torch.from_numpy(new))
+        w.fill_(-1.0)
+        g.replay()
+        got, o = w.clone(), out.clone()
+        w2 = torch.full_like(w, -1.0)
+        o2 = paged_attention_decode_weights(q, cache, gt, gl, 0.125, longest, w2, decay=0.0,
+                                            partition_tokens=pt)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w2) and torch.equal(o.view(torch.int16), o2.view(torch.int16))
+    assert pkv_check()[0] == 0
