@@ -49,26 +49,22 @@ struct RopeParams {
   uint8_t *k_cache, *v_cache;
   long long num_tokens, num_slots;
   int num_heads, num_kv_heads, num_axes, rotary_dim;
-  int splits;  // warps that share a token's heads
   float k_scale, v_scale;
 };
 
-// One warp takes a token's heads (or every splits-th group of them): q, k
-// and v heads in that order, 512 / D of them side by side.  A lane owns two
-// 8-element vectors of a head, the same two in every head, and with them the
-// 8 pairs they hold.  The token's angles are spread over the warp, two a
-// lane, and every lane collects the sines and cosines of its pairs once.
-// The first heads' loads go out before the angles are known, the next heads'
-// before the current ones are turned.
-template <bool FP8, int D, bool ADJACENT>
-__global__ void __launch_bounds__(kRopeThreads)
+// A token's heads (q, k and v heads in that order) are taken 512 / D side by
+// side, BATCH such groups at a time: a unit of work.  A warp takes a run of
+// consecutive units, so that the runs differ by one unit at most.  A lane
+// owns two 8-element vectors of a head, the same two in every head, and with
+// them the 8 pairs they hold.  The angles of a token are spread over the
+// warp, two a lane, and every lane collects the sines and cosines of its
+// pairs once a token.  The next unit's loads go out before the current one
+// is turned.  What bounds it is memory.
+template <bool FP8, int D, bool ADJACENT, int BATCH>
+__global__ void __launch_bounds__(kRopeThreads, 4)
     rope_write_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
   constexpr int LANES = D / 16;        // lanes of a head
   constexpr int HEADS = 32 / LANES;    // heads side by side
-  // head groups whose loads go out together: 4 of 4 heads or 2 of 8 (8192
-  // tokens of 48 heads of 128: 4 groups 35.8 us, 2 groups 37.8, 3 40.4; 1237
-  // tokens of 24 heads of 64: 4 groups 7.3 us, 2 groups 6.8)
-  constexpr int BATCH = D == 128 ? 4 : 2;
   const int lane = threadIdx.x & 31;
   const int sub = lane / LANES, u = lane % LANES;
   const bool turned = u < p.rotary_dim / 16;
@@ -84,42 +80,68 @@ __global__ void __launch_bounds__(kRopeThreads)
     axis[0] = table.axis[2 * lane], axis[1] = table.axis[2 * lane + 1];
   }
   const int q_end = p.num_heads, k_end = q_end + p.num_kv_heads, all = k_end + p.num_kv_heads;
-  const int groups = (all + HEADS - 1) / HEADS;
+  const int per_token = (all + HEADS * BATCH - 1) / (HEADS * BATCH);  // units
   const int row_vecs = p.num_kv_heads * (D / 8);
+
+  const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
+  const long long units = p.num_tokens * per_token;
+  const long long me = blockIdx.x * (long long)(kRopeThreads / 32) + (threadIdx.x >> 5);
+  // (units < 2^47, warps < 2^16)
+  const long long begin = units * me / warps, end = units * (me + 1) / warps;
+  long long tok = begin / per_token;
+  int unit = (int)(begin - tok * per_token);
 
   grid_dependency_wait();
   allow_dependent_launch();
+  if (begin >= end) return;
 
-  const long long warps = (long long)gridDim.x * (kRopeThreads / 32);
-  const long long items = p.num_tokens * p.splits;
-  for (long long item = blockIdx.x * (long long)(kRopeThreads / 32) + (threadIdx.x >> 5);
-       item < items; item += warps) {
-    const long long tok = p.splits == 1 ? item : item / p.splits;
-    const int first = (int)(item - tok * p.splits);
-    const int32_t my_pos =
-        lane < p.num_axes ? __ldg(p.positions + lane * p.axis_stride + tok) : 0;
-    const int64_t slot = __ldg(p.slots + tok);
-
-    uint4 a[BATCH], b[BATCH];
-    auto load = [&](int g0) {
+  int32_t next_pos = 0;
+  int64_t next_slot = 0;
+  auto load_token = [&](long long t) {
+    if (lane < p.num_axes) next_pos = __ldg(p.positions + lane * p.axis_stride + t);
+    next_slot = __ldg(p.slots + t);
+  };
+  uint4 a[BATCH], b[BATCH];
+  auto load = [&](long long t, int un) {
 #pragma unroll
-      for (int n = 0; n < BATCH; ++n) {
-        const int h = (g0 + n * p.splits) * HEADS + sub;
-        if (h >= all) continue;
-        const uint4 *src = h < q_end   ? p.q + tok * p.q_stride + h * (D / 8)
-                           : h < k_end ? p.k + tok * p.k_stride + (h - q_end) * (D / 8)
-                                       : p.v + tok * p.v_stride + (h - k_end) * (D / 8);
-        a[n] = src[v0];
-        b[n] = src[v1];
-      }
-    };
-    load(first);
+    for (int n = 0; n < BATCH; ++n) {
+      const int h = (un * BATCH + n) * HEADS + sub;
+      if (h >= all) continue;
+      const uint4 *src = h < q_end   ? p.q + t * p.q_stride + h * (D / 8)
+                         : h < k_end ? p.k + t * p.k_stride + (h - q_end) * (D / 8)
+                                     : p.v + t * p.v_stride + (h - k_end) * (D / 8);
+      a[n] = src[v0];
+      b[n] = src[v1];
+    }
+  };
+  load_token(tok);
+  load(tok, unit);
+  float cs[8], sn[8];
+  int64_t slot = 0;
+  bool put = false, new_token = true;
+  for (long long left = end - begin; left > 0; --left) {
+    const long long this_tok = tok;
+    const int this_unit = unit;
+    const bool first = new_token;
+    const int32_t my_pos = next_pos;
+    if (first) {
+      slot = next_slot;
+      put = slot >= 0 && slot < p.num_slots;
+      if (slot >= p.num_slots && this_unit == 0 && lane == 0)
+        record_error(&g_err_rope, PKV_ERR_RANGE, this_tok);
+    }
+    uint4 ca[BATCH], cb[BATCH];
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) ca[n] = a[n], cb[n] = b[n];
+    new_token = ++unit == per_token;
+    if (new_token) {
+      unit = 0;
+      ++tok;
+      if (left > 1) load_token(tok);
+    }
+    if (left > 1) load(tok, unit);
 
-    const bool put = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && first == 0 && lane == 0)
-      record_error(&g_err_rope, PKV_ERR_RANGE, tok);
-    float cs[8], sn[8];
-    {
+    if (first) {
       float c2[2], s2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -134,69 +156,63 @@ __global__ void __launch_bounds__(kRopeThreads)
       }
     }
 
-    for (int g0 = first; g0 < groups; g0 += BATCH * p.splits) {
-      uint4 ca[BATCH], cb[BATCH];
 #pragma unroll
-      for (int n = 0; n < BATCH; ++n) ca[n] = a[n], cb[n] = b[n];
-      load(g0 + BATCH * p.splits);
+    for (int n = 0; n < BATCH; ++n) {
+      const int h = (this_unit * BATCH + n) * HEADS + sub;
+      if (h >= all || (h >= q_end && !put)) continue;
+      float x[8], y[8];  // the vectors' elements
+      const uint32_t wa[4] = {ca[n].x, ca[n].y, ca[n].z, ca[n].w};
+      const uint32_t wb[4] = {cb[n].x, cb[n].y, cb[n].z, cb[n].w};
 #pragma unroll
-      for (int n = 0; n < BATCH; ++n) {
-        const int h = (g0 + n * p.splits) * HEADS + sub;
-        if (h >= all || (h >= q_end && !put)) continue;
-        float x[8], y[8];  // the vectors' elements
-        const uint32_t wa[4] = {ca[n].x, ca[n].y, ca[n].z, ca[n].w};
-        const uint32_t wb[4] = {cb[n].x, cb[n].y, cb[n].z, cb[n].w};
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(wa[i] << 16);
+        x[2 * i + 1] = __uint_as_float(wa[i] & 0xffff0000u);
+        y[2 * i] = __uint_as_float(wb[i] << 16);
+        y[2 * i + 1] = __uint_as_float(wb[i] & 0xffff0000u);
+      }
+      if (turned && h < k_end) {
+        if (ADJACENT) {  // vector a: pairs 0..3, vector b: pairs 4..7
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __uint_as_float(wa[i] << 16);
-          x[2 * i + 1] = __uint_as_float(wa[i] & 0xffff0000u);
-          y[2 * i] = __uint_as_float(wb[i] << 16);
-          y[2 * i + 1] = __uint_as_float(wb[i] & 0xffff0000u);
-        }
-        if (turned && h < k_end) {
-          if (ADJACENT) {  // vector a: pairs 0..3, vector b: pairs 4..7
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float s = x[2 * i], t = x[2 * i + 1];
-              x[2 * i] = s * cs[i] - t * sn[i];
-              x[2 * i + 1] = s * sn[i] + t * cs[i];
-              s = y[2 * i], t = y[2 * i + 1];
-              y[2 * i] = s * cs[4 + i] - t * sn[4 + i];
-              y[2 * i + 1] = s * sn[4 + i] + t * cs[4 + i];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float s = x[i], t = y[i];
-              x[i] = s * cs[i] - t * sn[i];
-              y[i] = s * sn[i] + t * cs[i];
-            }
+          for (int i = 0; i < 4; ++i) {
+            float s = x[2 * i], t = x[2 * i + 1];
+            x[2 * i] = s * cs[i] - t * sn[i];
+            x[2 * i + 1] = s * sn[i] + t * cs[i];
+            s = y[2 * i], t = y[2 * i + 1];
+            y[2 * i] = s * cs[4 + i] - t * sn[4 + i];
+            y[2 * i + 1] = s * sn[4 + i] + t * cs[4 + i];
           }
-        }
-        if (FP8 && h >= q_end) {
-          const bool is_k = h < k_end;
-          const float scale = is_k ? p.k_scale : p.v_scale;
-          const E4m3Recip r = e4m3_recip(scale);
-          uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) + slot * row_vecs +
-                       (h - (is_k ? q_end : k_end)) * (D / 8);
-          dst[v0] = quant8_e4m3(x, scale, r);
-          dst[v1] = quant8_e4m3(y, scale, r);
         } else {
-          uint4 *dst = h < q_end ? p.q_out + tok * p.out_stride + h * (D / 8)
-                       : h < k_end
-                           ? reinterpret_cast<uint4 *>(p.k_cache) + slot * row_vecs +
-                                 (h - q_end) * (D / 8)
-                           : reinterpret_cast<uint4 *>(p.v_cache) + slot * row_vecs +
-                                 (h - k_end) * (D / 8);
-          if (turned && h < k_end) {
-            ca[n] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-            cb[n] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float s = x[i], t = y[i];
+            x[i] = s * cs[i] - t * sn[i];
+            y[i] = s * sn[i] + t * cs[i];
           }
-          dst[v0] = ca[n];  // not turned: the bits unchanged
-          dst[v1] = cb[n];
         }
+      }
+      if (FP8 && h >= q_end) {
+        const bool is_k = h < k_end;
+        const float scale = is_k ? p.k_scale : p.v_scale;
+        const E4m3Recip r = e4m3_recip(scale);
+        uint2 *dst = reinterpret_cast<uint2 *>(is_k ? p.k_cache : p.v_cache) + slot * row_vecs +
+                     (h - (is_k ? q_end : k_end)) * (D / 8);
+        dst[v0] = quant8_e4m3(x, scale, r);
+        dst[v1] = quant8_e4m3(y, scale, r);
+      } else {
+        uint4 *dst = h < q_end ? p.q_out + this_tok * p.out_stride + h * (D / 8)
+                     : h < k_end
+                         ? reinterpret_cast<uint4 *>(p.k_cache) + slot * row_vecs +
+                               (h - q_end) * (D / 8)
+                         : reinterpret_cast<uint4 *>(p.v_cache) + slot * row_vecs +
+                               (h - k_end) * (D / 8);
+        if (turned && h < k_end) {
+          ca[n] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          cb[n] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                             pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        }
+        dst[v0] = ca[n];  // not turned: the bits unchanged
+        dst[v1] = cb[n];
       }
     }
   }
@@ -231,7 +247,7 @@ uint64_t turns_2_64(double f) {
   return ((uint64_t)hi << 32) + (uint64_t)lo + (uint64_t)std::llround(rest * 0x1p64);
 }
 
-template <bool FP8, int D>
+template <bool FP8, int D, int BATCH>
 cudaError_t launch_rope(bool adjacent, int grid, cudaStream_t s, const RopeTable &t,
                         const RopeParams &p) {
   cudaLaunchConfig_t cfg = {};
@@ -243,8 +259,27 @@ cudaError_t launch_rope(bool adjacent, int grid, cudaStream_t s, const RopeTable
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return adjacent ? cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, true>, t, p)
-                  : cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, false>, t, p);
+  return adjacent ? cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, true, BATCH>, t, p)
+                  : cudaLaunchKernelEx(&cfg, rope_write_kernel<FP8, D, false, BATCH>, t, p);
+}
+
+template <bool FP8, int D>
+cudaError_t launch_rope(bool adjacent, int64_t sms, cudaStream_t s, const RopeTable &t,
+                        const RopeParams &p) {
+  constexpr int kWarps = kRopeThreads / 32;
+  // Groups of heads in a unit where every warp of the GPU gets one, and four
+  // CTAs an SM: 8192 tokens of 48 heads of 128 took 34.9 us with 2 groups,
+  // 34.1 with 3, 40.6 with 4 (132 registers: three CTAs), and 36 to 39 with
+  // more CTAs of less; a warp a token, 4 groups at a time, 36.0.  Fewer tokens
+  // go a group at a time to as many warps.
+  constexpr int BATCH = D == 128 ? 3 : 2;
+  const int64_t heads = p.num_heads + 2 * (int64_t)p.num_kv_heads, side = 512 / D;
+  const int64_t units = p.num_tokens * ((heads + side * BATCH - 1) / (side * BATCH));
+  if (units >= sms * 4 * kWarps)
+    return launch_rope<FP8, D, BATCH>(adjacent, (int)(sms * 4), s, t, p);
+  const int64_t single = p.num_tokens * ((heads + side - 1) / side);
+  const int64_t grid = std::min<int64_t>((single + kWarps - 1) / kWarps, sms * 8);
+  return launch_rope<FP8, D, 1>(adjacent, (int)grid, s, t, p);
 }
 
 }  // namespace
@@ -336,22 +371,14 @@ extern "C" pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const
   p.rotary_dim = R;
   p.k_scale = fp8 ? cache->k_scale : 1.f;
   p.v_scale = fp8 ? cache->v_scale : 1.f;
-  // Few tokens: a token's head groups go to several warps, up to one each.
-  const int64_t heads = num_heads + 2 * (int64_t)cache->num_kv_heads;
-  const int64_t groups = (heads + 512 / D - 1) / (512 / D);
-  const int64_t target = (int64_t)sms * 32;
-  p.splits = (int)std::min<int64_t>(groups, std::max<int64_t>(1, target / num_tokens));
-  const int64_t warps = num_tokens * p.splits;
-  const int64_t want = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  const int grid = (int)std::min<int64_t>(want, (int64_t)sms * 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool adj = rope->interleaved != 0;
   cudaError_t e;
   if (fp8)
-    e = D == 128 ? launch_rope<true, 128>(adj, grid, s, t, p)
-                 : launch_rope<true, 64>(adj, grid, s, t, p);
+    e = D == 128 ? launch_rope<true, 128>(adj, sms, s, t, p)
+                 : launch_rope<true, 64>(adj, sms, s, t, p);
   else
-    e = D == 128 ? launch_rope<false, 128>(adj, grid, s, t, p)
-                 : launch_rope<false, 64>(adj, grid, s, t, p);
+    e = D == 128 ? launch_rope<false, 128>(adj, sms, s, t, p)
+                 : launch_rope<false, 64>(adj, sms, s, t, p);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -242,11 +242,16 @@ def test_non_finite_values_stay_in_their_pair():
     assert torch.equal(bad, want)
 
 
-def test_large_batch_takes_every_token():
-    """More tokens than the grid has warps: the grid-stride path."""
-    T = 20011
-    rng, q, k, v, cache, slots = _make(T, 2, 1, 64, seed=12)
-    rope = RotaryAxes(64, [16, 16])
+@pytest.mark.parametrize("T,Hq,Hkv,D,kv_dtype", [
+    (20011, 2, 1, 64, "bf16"), (2431, 4, 2, 128, "bf16"), (2433, 4, 2, 128, "fp8_e4m3"),
+    (1300, 20, 5, 128, "bf16"), (1217, 17, 8, 64, "fp8_e4m3"), (4000, 1, 1, 128, "bf16")])
+def test_many_tokens_take_every_unit(T, Hq, Hkv, D, kv_dtype):
+    """Warps with runs of several units, tokens cut between two warps, last
+    units of a token partly empty."""
+    rng, q, k, v, cache, slots = _make(T, Hq, Hkv, D, kv_dtype, seed=12)
+    slots[T // 2] = -1
+    slots[T - 1] = -1
+    rope = RotaryAxes(D, [D // 4, D // 4])
     pos = torch.from_numpy(rng.integers(0, 1 << 20, (2, T)).astype(np.int32)).cuda()
     qo = paged_kv_rope_write(q, k, v, pos, slots, cache, rope)
     _check(q, k, v, qo, cache, slots, pos, rope)
