@@ -178,7 +178,7 @@ pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const void *k,
  *                 n on the host.
  *   per_head      non-zero: every kv head chooses by its own weights; zero:
  *                 all heads keep the same tokens, chosen by the heads' sum
- *                 (added in binary64, rounded once to binary32).
+ *                 (carried to 48 bits, rounded once to binary32).
  *   dst_tables    NULL: in place (the sequence's blocks must then be its
  *                 own, shared with no other sequence); otherwise int32
  *                 [batch, dst_max_blocks]: position i goes to row i % 16 of

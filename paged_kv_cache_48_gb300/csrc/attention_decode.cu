@@ -1309,11 +1309,17 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
 // Running attention weights: weights[b, kvh, t] = decay * weights[b, kvh, t]
 // + sum over the kv head's query heads h of 2^(s_ht - M_h) / l_h, from the
 // kept scores s and each row's partition statistics (m_j, l_j), M = max m_j,
-// l = sum 2^(m_j - M) l_j.  A CTA takes a run of kAccTokens-token chunks of
-// one (sequence, kv head): the statistics once, then chunk by chunk all the
-// scores of a thread's tokens loaded before the first is used, so that what
-// bounds it is memory.  A thread owns its tokens and every sum has a fixed
-// order.
+// l = sum 2^(m_j - M) l_j.  A token's weight needs the statistics of its whole
+// row, which are known when the last partition is done, so the decode kernel
+// keeps its scores: in binary32 (the weights' error is the scores'), 4 bytes a
+// query head and token written and read, 32 to 64 bytes beside the 256 to 512
+// of a kv head's K and V; forming them again would read K, half the cache, a
+// second time.  A CTA takes a run of kAccTokens-token chunks of one (sequence,
+// kv head): the statistics once, then chunk by chunk all the scores of a
+// thread's tokens loaded before the first is used, so that what bounds it is
+// memory: 128 E4M3 sequences (151 MB of scores and weights) 31 us, 4.9 TB/s;
+// eight long contexts (210 MB) 39 us, 5.4 TB/s.  With a CTA a chunk they took
+// 40 and 54 us.  A thread owns its tokens and every sum has a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kAccThreads = 256;
 constexpr int kAccPerThread = 4;
