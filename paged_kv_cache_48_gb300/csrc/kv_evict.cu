@@ -779,8 +779,10 @@ extern "C" pkv_status paged_kv_evict(const pkv_cache *cache, const int32_t *bloc
     return PKV_ERR_ARG;
   if (batch == 0) return PKV_OK;
   if (!block_tables || !seq_lens || !weights || !keep || !new_seq_lens) return PKV_ERR_ARG;
-  if (batch > 65535 || cache->num_kv_heads > 65535 || weights_stride > INT32_MAX ||
-      (dst_weights && dst_weights_stride > INT32_MAX) || max_keep > INT32_MAX - 1024)
+  // grid limits, and positions with room for 32-bit index arithmetic
+  constexpr int64_t kMost = INT64_C(1) << 30;
+  if (batch > 65535 || cache->num_kv_heads > 65535 || weights_stride > kMost ||
+      (dst_weights && dst_weights_stride > kMost) || max_keep > kMost)
     return PKV_ERR_ARG;
   const size_t rows = (size_t)batch * cache->num_kv_heads;
   // other weights must not lie over the ones still to be read

@@ -316,9 +316,9 @@ extern "C" pkv_status paged_kv_rope_write(const void *q, int64_t q_stride, const
   if (!k || !v || !positions || !slot_mapping || (num_heads > 0 && (!q || !q_out)))
     return PKV_ERR_ARG;
   const int64_t q_len = (int64_t)num_heads * D, kv_len = (int64_t)cache->num_kv_heads * D;
-  // bounds under which no byte offset below overflows
+  // bounds under which no byte offset and no unit count overflows
   constexpr int64_t kMaxStride = INT64_C(1) << 30;
-  if (num_heads > INT32_MAX / 4 || cache->num_kv_heads > INT32_MAX / 8 || num_tokens > INT32_MAX ||
+  if (num_heads > 65535 || cache->num_kv_heads > 65535 || num_tokens > INT32_MAX ||
       k_stride > kMaxStride || v_stride > kMaxStride ||
       (num_heads > 0 && (q_stride > kMaxStride || q_out_stride > kMaxStride)))
     return PKV_ERR_ARG;

@@ -38,6 +38,7 @@ def _rope_call(lib, q=1 << 20, qs=256, k=1 << 21, ks=256, v=1 << 22, vs=256, pos
     (dict(rope=False), ARG),
     (dict(T=-1), ARG),
     (dict(heads=-1), ARG),
+    (dict(heads=65536, qs=1 << 24, os=1 << 24), ARG),
     (dict(k=None), ARG),
     (dict(v=None), ARG),
     (dict(q=None), ARG),
@@ -173,6 +174,8 @@ def _evict_call(lib, cache=None, max_blocks=8, lens=1 << 16, w=1 << 20, stride=1
     (dict(sink=-1), ARG),
     (dict(recent=-1), ARG),
     (dict(stride=-1), ARG),
+    (dict(stride=1 << 31), ARG),
+    (dict(max_keep=(1 << 30) + 1), ARG),
     (dict(max_blocks=0), ARG),
     (dict(dst=1 << 21, dmb=0), ARG),
     (dict(dw=(1 << 20) + 64, dstride=64), ARG),   # over the weights still to be read
