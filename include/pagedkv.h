@@ -387,9 +387,9 @@ pkv_status paged_attention_decode_step(const void *q, const void *k_new,
  * paged_attention_decode, or paged_attention_decode_step with new tokens.
  * Weights are binary32 sums in a fixed order; a token excluded from the
  * softmax (its block outside the pool, its wait timed out) gains 0.  A NaN
- * score (NaN or opposing infinities in q or in a cached key of the sequence)
- * makes its row of out and its kv head's weights NaN, as the formula does;
- * paged_attention_decode may write 0 there. */
+ * or +infinite score (NaN or an infinity in q or in a cached key of the
+ * sequence) makes its row of out and its kv head's weights NaN, as the formula
+ * does; paged_attention_decode may write 0 there. */
 pkv_status paged_attention_decode_weights(
     const void *q, const void *k_new, const void *v_new,
     const int32_t *new_start_loc, int64_t num_new_tokens,

@@ -37,6 +37,9 @@
 // zeroing of a freshly allocated block), and the host side of shared-prefix
 // (cascade) decode: the tensor-core prefix pass (attention_prefill.cu), this
 // kernel over each sequence's own tokens launched beside it, and the merge.
+// And decode that keeps running attention weights, the measure eviction goes
+// by (kv_evict.cu): the kernel also stores its scores, and a second launch
+// turns them into weights when every row's statistics are known.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -692,9 +695,9 @@ __device__ __forceinline__ void write_new_rows(const DecodeParams &p, int blk, i
 // Decode kernel
 // ===========================================================================
 // WEIGHTS: every score is also kept in p.logits, and every row's (max, sum)
-// in p.part_ml, split or not, for weights_finish_kernel; and a NaN score
-// makes its row NaN, as the formula does (a NaN sum is carried through, also
-// past a maximum of -inf), where the other kernels write 0.
+// in p.part_ml, split or not, for weights_finish_kernel; and a NaN or +inf
+// score makes its row NaN, as the formula does (a NaN sum is carried through,
+// also past a maximum of -inf), where the other kernels may write 0.
 template <bool FP8, int D, bool WEIGHTS = false, int NW = 4, int RING_KB = 64>
 __global__ void __launch_bounds__(NW * 32)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
