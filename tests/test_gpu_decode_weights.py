@@ -184,7 +184,8 @@ def test_weights_sum_to_the_heads():
                                    decay=0.0)
     valid = torch.arange(W.max_seq_len, device="cuda") < G.seq_lens[:, None]
     s = torch.where(valid[:, None], w, 0.0).double().sum(-1)
-    # every weight is off by under 2^-10 of itself here (scores below 100)
+    # lifetime_ref.weights_tolerance with |q| . |k| scale below 24 (128 products
+    # of N(0, 1) values average 7.2) and 400 tokens: 7.7e-4, below 2^-10
     assert ((s - W.group_size).abs() <= W.group_size * 2.0 ** -10).all()
 
 

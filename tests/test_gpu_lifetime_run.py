@@ -394,3 +394,120 @@ def test_workspace_past_two_gigabytes():
     assert torch.allclose(w[idx][:, :, :336], w2, rtol=1e-5, atol=0)
     assert torch.allclose(out[idx].float(), o2.float(), rtol=2e-2, atol=2e-3)
     assert not bool(w[:, :, 336:].any()) and not bool(w[1:40].any())
+
+
+def test_largest_batch():
+    """65535 sequences, the grid's limit, of 1 to 20 tokens."""
+    B, D = 65535, 64
+    lens = (np.arange(B) % 20 + 1).astype(np.int32)
+    order = torch.randperm(2 * B, device="cuda").to(torch.int32).view(B, 2)
+    cache = PagedKVCache.empty(2 * B, 1, D)
+    cache.key_cache.normal_()
+    cache.value_cache.normal_()
+    gl = _dev(lens)
+    q = torch.randn(B, 1, D, device="cuda").bfloat16()
+    w = torch.zeros(B, 1, 20, device="cuda")
+    out = paged_attention_decode_weights(q, cache, order, gl, 0.125, 20, w)
+    t = torch.arange(20, device="cuda")
+    slots = order.long()[:, t // 16] * 16 + t % 16
+    k = cache.key_cache.view(-1, D)[slots].double()
+    v = cache.value_cache.view(-1, D)[slots].double()
+    s = torch.einsum("bd,btd->bt", q[:, 0].double(), k) * 0.125
+    s[t >= gl[:, None]] = float("-inf")
+    p = torch.softmax(s, -1)
+    bound = float((torch.einsum("bd,btd->bt", q[:, 0].double().abs(), k.abs()) * 0.125).max())
+    tol = ref.weights_tolerance(D, 20, 1, bound)
+    assert bool(((w[:, 0].double() - p).abs() <= tol * p + 1e-37).all())
+    ref_out = torch.einsum("bt,btd->bd", p, torch.where((t < gl[:, None])[:, :, None], v, 0.0))
+    assert bool(((out[:, 0].double() - ref_out).abs() <= 1e-2 + 1e-2 * ref_out.abs()).all())
+    keep = torch.full((B,), 7, dtype=torch.int32, device="cuda")
+    old = w.clone()
+    before = cache.key_cache.view(-1, D)[slots].clone()
+    kept = torch.empty(B, 1, 7, dtype=torch.int32, device="cuda")
+    new = paged_kv_evict(cache, order, gl, w, keep, 7, sink=1, recent=2, kept=kept)
+    assert pkv_check()[0] == 0
+    assert torch.equal(new, torch.clamp(gl, max=7))
+    at = kept[:, 0].long()
+    live = at >= 0
+    assert torch.equal(live.sum(-1).int(), new)
+    got = cache.key_cache.view(-1, D)[slots[:, :7]]
+    want = torch.gather(before, 1, at.clamp(min=0)[:, :, None].expand(-1, -1, D))
+    assert torch.equal(got[live].view(torch.int16), want[live].view(torch.int16))
+    assert torch.equal(w[:, 0, :7][live], torch.gather(old[:, 0], 1, at.clamp(min=0))[live])
+    for b in (0, 6, 7, 8, 19, 65534):
+        assert at[b][live[b]].tolist() == ref.evict_choice(old[b, 0].cpu().numpy(), int(lens[b]), 7,
+                                                           1, 2)
+
+
+@pytest.mark.parametrize("per_head", [True, False])
+def test_many_kv_heads(per_head):
+    """300 kv heads with a query head each."""
+    H, D, L = 300, 64, 90
+    cache = PagedKVCache.empty(12, H, D)
+    rng = np.random.default_rng(2)
+    tables = rng.permutation(12).astype(np.int32).reshape(2, 6)
+    slots = np.array([int(tables[b, t // 16]) * 16 + t % 16 for b in range(2) for t in range(L)])
+    q, k, v = (torch.randn(2 * L, H, D, device="cuda").bfloat16() for _ in range(3))
+    pos = torch.arange(2 * L, dtype=torch.int32, device="cuda")
+    rope = RotaryAxes(D, [32])
+    qr = paged_kv_rope_write(q, k, v, pos, _dev(slots), cache, rope)
+    want, mag = ref.rotate(q[:3].float().cpu().numpy().astype(np.float64), np.arange(3)[None],
+                           rope.frequencies, rope.axis, D, False)
+    got = qr[:3].float().cpu().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + mag * 2.0 ** -21).all()
+    lens = torch.tensor([L, L], dtype=torch.int32, device="cuda")
+    w = torch.zeros(2, H, L, device="cuda")
+    paged_attention_decode_weights(qr[:2].contiguous(), cache, _dev(tables), lens, 0.125, L, w)
+    old = w.cpu().numpy()
+    for b in range(2):
+        kk = cache.key_cache.view(-1, H, D)[_dev(slots[b * L:(b + 1) * L])].double()
+        p = torch.softmax(torch.einsum("hd,thd->ht", qr[b].double(), kk) * 0.125, -1)
+        bound = float((torch.einsum("hd,thd->ht", qr[b].double().abs(), kk.abs()) * 0.125).max())
+        tol = ref.weights_tolerance(D, L, 1, bound)
+        assert bool(((w[b].double() - p).abs() <= tol * p + 1e-37).all())
+    kept = torch.empty(2, H if per_head else 1, 33, dtype=torch.int32, device="cuda")
+    paged_kv_evict(cache, _dev(tables), lens, w, _dev(np.array([33, 20], np.int32)), 33, sink=3,
+                   recent=5, per_head=per_head, kept=kept)
+    assert pkv_check()[0] == 0
+    for b, n in ((0, 33), (1, 20)):
+        for h in (0, 1, 150, 299):
+            rank = old[b, h] if per_head else ref.heads_sum(old[b])
+            at = ref.evict_choice(rank, L, n, 3, 5)
+            assert kept[b, h if per_head else 0, :n].tolist() == at
+            d = np.array([int(tables[b, i // 16]) * 16 + i % 16 for i in range(n)])
+            assert torch.equal(cache.value_cache.view(-1, H, D)[_dev(d), h],
+                               v[b * L:(b + 1) * L, h][_dev(np.array(at))])
+
+
+def test_host_threads_call_at_once():
+    """Four host threads, a stream and a state each."""
+    import threading
+    states, alone = [_loop_state(10 + i) for i in range(4)], [_loop_state(10 + i) for i in range(4)]
+    for X, E in zip(states, alone):
+        for n in ("weights", "q", "k", "v"):
+            E[n].copy_(X[n])
+        E["cache"].key_cache.copy_(X["cache"].key_cache)
+        E["cache"].value_cache.copy_(X["cache"].value_cache)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(X):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(25):
+                _loop_step(X, stream=s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(X,)) for X in states]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for _ in range(25):
+        for E in alone:
+            _loop_step(E)
+    for X, E in zip(states, alone):
+        assert _same(_result(X), _result(E))
+    assert pkv_check()[0] == 0
