@@ -127,6 +127,9 @@ struct DecodeParams {
   // 1: no sequence is split and a CTA holds all query heads of its kv head,
   // so the decode kernel adds the weights itself and no second launch follows
   int32_t weights_inline;
+  // 1: the scores stay in L2 (evict_last) until the finishing launch has used
+  // them and drops them there, so that they never reach DRAM
+  int32_t scores_in_l2;
   float decay;
 };
 
@@ -347,13 +350,34 @@ __device__ __forceinline__ void block_scores(uint32_t sk,
   for (int i = 0; i < 4; ++i) sc[i] = sa[i] + sb[i];
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_last() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;"
+               : "=l"(p));
+  return p;
+}
+
 // WEIGHTS kernels: a block's 16 scores of heads 2c, 2c+1 (this lane's tokens
 // g and g + 8) to its [16][heads] piece of the unit's kept scores.
-__device__ __forceinline__ void keep_scores(float *lg, int heads, int g, int c, float s0, float s1,
+struct Keep {
+  int heads;        // scores of a token
+  uint64_t policy;  // of the stores in L2; 0: the usual one
+};
+
+__device__ __forceinline__ void store_scores(float *a, float x, float y, uint64_t policy) {
+  if (policy)
+    asm volatile("st.global.L2::cache_hint.v2.f32 [%0], {%1, %2}, %3;" ::"l"(a), "f"(x), "f"(y),
+                 "l"(policy)
+                 : "memory");
+  else
+    *reinterpret_cast<float2 *>(a) = make_float2(x, y);
+}
+
+__device__ __forceinline__ void keep_scores(float *lg, Keep keep, int g, int c, float s0, float s1,
                                             float s2, float s3) {
-  if (2 * c < heads) {
-    *reinterpret_cast<float2 *>(lg + g * heads + 2 * c) = make_float2(s0, s1);
-    *reinterpret_cast<float2 *>(lg + (g + 8) * heads + 2 * c) = make_float2(s2, s3);
+  if (2 * c < keep.heads) {
+    store_scores(lg + g * keep.heads + 2 * c, s0, s1, keep.policy);
+    store_scores(lg + (g + 8) * keep.heads + 2 * c, s2, s3, keep.policy);
   }
 }
 
@@ -362,7 +386,7 @@ __device__ __forceinline__ void keep_scores(float *lg, int heads, int g, int c, 
 template <bool FP8, int D, bool FULL, bool WEIGHTS>
 __device__ __forceinline__ void block_update(uint32_t sv, int nv, const float (&sc)[4],
                                              float scale_log2, WarpState<FP8, D> &st, int lane,
-                                             float *lg, int lg_heads,
+                                             float *lg, Keep keep,
                                              uint32_t box_stride = 16 * Cfg<FP8, D>::BOX_BYTES) {
   using C = Cfg<FP8, D>;
   const int g = lane >> 2, c = lane & 3;
@@ -378,7 +402,7 @@ __device__ __forceinline__ void block_update(uint32_t sv, int nv, const float (&
   const float s1 = v_lo ? sc[1] * scale_log2 : -INFINITY;
   const float s2 = v_hi ? sc[2] * scale_log2 : -INFINITY;
   const float s3 = v_hi ? sc[3] * scale_log2 : -INFINITY;
-  if constexpr (WEIGHTS) keep_scores(lg, lg_heads, g, c, s0, s1, s2, s3);
+  if constexpr (WEIGHTS) keep_scores(lg, keep, g, c, s0, s1, s2, s3);
   float bm0 = fmaxf(s0, s2), bm1 = fmaxf(s1, s3);
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
@@ -459,13 +483,13 @@ template <bool FP8, int D, bool WEIGHTS>
 __device__ __forceinline__ void attend_block(uint32_t sk, uint32_t sv, int nv,
                                              const uint32_t (&qf)[Cfg<FP8, D>::MT][2],
                                              float scale_log2, WarpState<FP8, D> &st,
-                                             int lane, float *lg, int lg_heads) {
+                                             int lane, float *lg, Keep keep) {
   float sc[4];
   block_scores<FP8, D>(sk, qf, sc, lane);
   if (nv == 16)
-    block_update<FP8, D, true, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, lg_heads);
+    block_update<FP8, D, true, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, keep);
   else
-    block_update<FP8, D, false, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, lg_heads);
+    block_update<FP8, D, false, WEIGHTS>(sv, nv, sc, scale_log2, st, lane, lg, keep);
 }
 
 // fp8 caches: two 16-token blocks per online-softmax step.  Their scores
@@ -476,7 +500,7 @@ template <int D, bool FULL, bool WEIGHTS>
 __device__ __forceinline__ void pair_update(uint32_t sva, int nva, const float (&sa)[4],
                                             uint32_t svb, int nvb, const float (&sb)[4],
                                             float scale_log2, WarpState<true, D> &st, int lane,
-                                            float *lga, float *lgb, int lg_heads) {
+                                            float *lga, float *lgb, Keep keep) {
   using C = Cfg<true, D>;
   const int g = lane >> 2, c = lane & 3;
   const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -492,8 +516,8 @@ __device__ __forceinline__ void pair_update(uint32_t sva, int nva, const float (
   const float t2 = b_hi ? sb[2] * scale_log2 : -INFINITY;
   const float t3 = b_hi ? sb[3] * scale_log2 : -INFINITY;
   if constexpr (WEIGHTS) {
-    keep_scores(lga, lg_heads, g, c, s0, s1, s2, s3);
-    keep_scores(lgb, lg_heads, g, c, t0, t1, t2, t3);
+    keep_scores(lga, keep, g, c, s0, s1, s2, s3);
+    keep_scores(lgb, keep, g, c, t0, t1, t2, t3);
   }
   float bm0 = fmaxf(fmaxf(s0, s2), fmaxf(t0, t2)), bm1 = fmaxf(fmaxf(s1, s3), fmaxf(t1, t3));
 #pragma unroll
@@ -564,17 +588,17 @@ template <int D, bool WEIGHTS>
 __device__ __forceinline__ void attend_pair(uint32_t ska, int nva, uint32_t skb, int nvb,
                                             const uint32_t (&qf)[Cfg<true, D>::MT][2],
                                             float scale_log2, WarpState<true, D> &st,
-                                            int lane, float *lga, float *lgb, int lg_heads) {
+                                            int lane, float *lga, float *lgb, Keep keep) {
   using C = Cfg<true, D>;
   float sa[4], sb[4];
   block_scores<true, D>(ska, qf, sa, lane);
   block_scores<true, D>(skb, qf, sb, lane);
   if (nva == 16 && nvb == 16)
     pair_update<D, true, WEIGHTS>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb,
-                                  scale_log2, st, lane, lga, lgb, lg_heads);
+                                  scale_log2, st, lane, lga, lgb, keep);
   else
     pair_update<D, false, WEIGHTS>(ska + C::TILE_BYTES, nva, sa, skb + C::TILE_BYTES, nvb, sb,
-                                   scale_log2, st, lane, lga, lgb, lg_heads);
+                                   scale_log2, st, lane, lga, lgb, keep);
 }
 
 // Lane 0 issues the TMA loads of one block-head (K and V tiles) into a
@@ -871,7 +895,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     else
       return nullptr;
   };
-  const int lg_heads = WEIGHTS ? p.logit_heads : 0;
+  Keep keep = {0, 0ull};
+  if constexpr (WEIGHTS)
+    keep = {p.logit_heads, p.scores_in_l2 ? l2_policy_evict_last() : 0ull};
 
   bool failed = false;
   int i = 0;
@@ -890,7 +916,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int nvb = stage_ok[warp][sb] ? min(16, tok1 - jb * 16) : 0;
       attend_pair<D, WEIGHTS>(smem_u32(ring + sa * C::STAGE_BYTES), nva,
                               smem_u32(ring + sb * C::STAGE_BYTES), nvb, qf, p.scale_log2, st,
-                              lane, lg_at(ja), lg_at(jb), lg_heads);
+                              lane, lg_at(ja), lg_at(jb), keep);
       __syncwarp();
       if (issued < my_n) issue(issued++);
       if (issued < my_n) issue(issued++);
@@ -906,7 +932,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int nv = stage_ok[warp][stage] ? min(16, tok1 - j * 16) : 0;
     const uint32_t sk = smem_u32(ring + stage * C::STAGE_BYTES);
     attend_block<FP8, D, WEIGHTS>(sk, sk + C::TILE_BYTES, nv, qf, p.scale_log2, st, lane, lg_at(j),
-                                  lg_heads);
+                                  keep);
     __syncwarp();
     if (issued < my_n) issue(issued++);
   }
@@ -923,7 +949,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if constexpr (WEIGHTS) {
       st.l0 = st.l1 = 0.f;
       for (int i = 0; i < my_n; ++i)
-        keep_scores(lg_at(blk0 + j_off + i * jstep), lg_heads, g, c, -INFINITY, -INFINITY,
+        keep_scores(lg_at(blk0 + j_off + i * jstep), keep, g, c, -INFINITY, -INFINITY,
                     -INFINITY, -INFINITY);
     }
   }
@@ -1317,7 +1343,9 @@ paged_decode_merge_wide_kernel(const DecodeParams p) {
 // keeps its scores: in binary32 (the weights' error is the scores'), 4 bytes a
 // query head and token written and read, 32 to 64 bytes beside the 256 to 512
 // of a kv head's K and V; forming them again would read K, half the cache, a
-// second time.  A CTA takes a run of kAccTokens-token chunks of one (sequence,
+// second time.  Where all of a call's scores fit in L2 they are stored
+// evict_last and their lines are discarded after use, so that none is written
+// to DRAM.  A CTA takes a run of kAccTokens-token chunks of one (sequence,
 // kv head): the statistics once, then chunk by chunk all the scores of a
 // thread's tokens loaded before the first is used, so that what bounds it is
 // memory: 128 E4M3 sequences (151 MB of scores and weights) 31 us, 4.9 TB/s;
@@ -1328,6 +1356,13 @@ constexpr int kAccThreads = 256;
 constexpr int kAccPerThread = 4;
 constexpr int kAccTokens = kAccThreads * kAccPerThread;
 constexpr int kAccHeads = 128;  // heads whose statistics a pass holds
+
+// Scores about to be discarded are read as usual; others are read as data that
+// is not needed again (E4M3 252 us a call, 261 without).
+template <typename T>
+__device__ __forceinline__ T last_load(const T *a, bool in_l2) {
+  return in_l2 ? __ldcg(a) : __ldcs(a);
+}
 
 // HP: scores of a token in a unit (heads of a sub-group, rounded up to even).
 template <int HP>
@@ -1343,6 +1378,7 @@ __device__ __forceinline__ void accumulate_weights(const DecodeParams &p, int b,
   const int nparts = L <= p.part_tokens ? 1 : (L + p.part_tokens - 1) / p.part_tokens;
   const int fresh = first_fresh(p, b, L_in, L);
   float *w = p.weights + ((size_t)b * p.num_kv_heads + kvh) * p.weights_stride;
+  const bool in_l2 = p.scores_in_l2;
   for (int h0 = 0; h0 < p.group; h0 += kAccHeads) {  // (one pass up to 128 heads a kv head)
     const int pass_heads = min(kAccHeads, p.group - h0);
     for (int h = warp; h < pass_heads; h += kAccThreads / 32) {
@@ -1385,13 +1421,15 @@ __device__ __forceinline__ void accumulate_weights(const DecodeParams &p, int b,
           if constexpr (HP % 4 == 0) {
 #pragma unroll
             for (int h = 0; h < HP; h += 4) {
-              const float4 v = __ldcs(reinterpret_cast<const float4 *>(lg + (size_t)t * HP + h));
+              const float4 v =
+                  last_load(reinterpret_cast<const float4 *>(lg + (size_t)t * HP + h), in_l2);
               s[k][h] = v.x, s[k][h + 1] = v.y, s[k][h + 2] = v.z, s[k][h + 3] = v.w;
             }
           } else {
 #pragma unroll
             for (int h = 0; h < HP; h += 2) {
-              const float2 v = __ldcs(reinterpret_cast<const float2 *>(lg + (size_t)t * HP + h));
+              const float2 v =
+                  last_load(reinterpret_cast<const float2 *>(lg + (size_t)t * HP + h), in_l2);
               s[k][h] = v.x, s[k][h + 1] = v.y;
             }
           }
@@ -1410,7 +1448,19 @@ __device__ __forceinline__ void accumulate_weights(const DecodeParams &p, int b,
         if (t < t_end) w[t] = (decay != 0.f ? decay * old[k] : 0.f) + acc[k];
       }
     }
-    __syncthreads();  // stat is reused by the next pass
+    __syncthreads();  // the scores are used; stat is reused by the next pass
+    if (in_l2) {
+      // a block's 16 tokens take HP * 64 bytes, whole lines, and runs begin and
+      // end at blocks' ends: these lines hold this run's scores alone
+      const int tokens = ((t_end + 15) & ~15) - t_begin;
+      const size_t bytes = (size_t)tokens * HP * sizeof(float);  // a multiple of 128
+      for (int g0 = 0; g0 < pass_heads; g0 += 8) {
+        const char *a = reinterpret_cast<const char *>(
+            lg0 + ((size_t)(g0 / 8) * p.logit_tokens + t_begin) * HP);
+        for (size_t o = (size_t)threadIdx.x * 128; o < bytes; o += (size_t)kAccThreads * 128)
+          asm volatile("discard.global.L2 [%0], 128;" ::"l"(a + o) : "memory");
+      }
+    }
   }
 }
 
@@ -1535,6 +1585,14 @@ constexpr int kMergeWarpMaxParts = 8;
 // with the second launch, 64 of 256 17.1 against 17.4; but 180 of 1000 tokens
 // 156 against 136, where a CTA's four warps alone would add up its tokens.
 constexpr int kInlineTokens = 256;
+
+// Scores of at most this many bytes (if every sequence had the bound's length)
+// stay in L2 (DecodeParams::scores_in_l2): half of its 129 MB, beside the
+// stream.  us a call in a row, written out and kept in L2: bf16 32 MB 108 and
+// 105, 64 MB 206 and 202, 128 MB (groups of eight) 239 and 237, 192 MB 587 and
+// 581; E4M3 in groups of five 48 MB 73.2 and 72.3, 96 MB 127.6 and 129.6,
+// 192 MB 243 and 248.
+constexpr size_t kScoresInL2 = size_t(64) << 20;
 
 // Partitions this short are owned by single warps (DecodeParams::warp_parts).
 constexpr int kWarpPartMaxTokens = 512;
@@ -1780,6 +1838,7 @@ pkv_status decode_entry(const void *q, const void *k_new, const void *v_new,
     p.weights_stride = weights_stride;
     p.decay = decay;
     p.weights_inline = parts64 == 1 && group <= 8 && max_seq_len <= kInlineTokens;
+    p.scores_in_l2 = !p.weights_inline && l.bytes - l.logits_off <= kScoresInL2;
   } else if (need > 0) {
     if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_ERR_WORKSPACE;

@@ -493,3 +493,40 @@ def test_replayed_with_other_queries_and_lengths():
         torch.cuda.synchronize()
         assert torch.equal(got, w2) and torch.equal(o.view(torch.int16), o2.view(torch.int16))
     assert pkv_check()[0] == 0
+
+
+@pytest.mark.parametrize("Hq,D,kv_dtype", [(64, 128, "bf16"), (40, 64, "fp8_e4m3"),
+                                           (24, 128, "bf16"), (88, 64, "bf16")])
+def test_the_bound_does_not_change_the_weights(Hq, D, kv_dtype):
+    """The same sequences under a bound that lets their scores fit in L2 and
+    under one that does not: weights bit for bit, and the workspace is used
+    again by the next call."""
+    B, Hkv, longest, pt = 64, 8, 1100, 1024
+    lens = [1, 0, 16, 17, 1024, 1025, 1099] + list(range(40, 40 + 18 * (B - 8), 18)) + [longest]
+    cache, q, tables, lens = _many(B, Hq, Hkv, D, lens, kv_dtype, seed=9)
+    gt, gl = torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda()
+    group = Hq // Hkv
+    units = (group + 7) // 8
+    heads = (min(8, group) + 1) // 2 * 2
+    results = []
+    for megabytes in (0, 100):
+        tokens = max(longest, (megabytes << 20) // (B * Hkv * units * heads * 4) + 1)
+        need = paged_attention_decode_weights_workspace_bytes(B, Hq, Hkv, D, tokens, pt)
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+        w = torch.zeros(B, Hkv, tokens, device="cuda")
+        for _ in range(3):
+            out = paged_attention_decode_weights(q, cache, gt, gl, 0.125, tokens, w, decay=0.5,
+                                                 partition_tokens=pt, workspace=ws)
+        plain = paged_attention_decode(q, cache, gt, gl, 0.125, max_seq_len=tokens,
+                                       partition_tokens=pt)
+        assert torch.equal(out.view(torch.int16), plain.view(torch.int16))
+        assert not bool(w[:, :, longest:].any())
+        results.append(w[:, :, :longest].clone())
+    assert torch.equal(results[0], results[1])
+    sums = results[0].double().sum(-1).cpu().numpy()
+    # 1 + 1/2 + 1/4 of a softmax a query head; statistics and weights come from
+    # the same scores, so what is left is the binary32 sum of at most 1100
+    # terms (1100 * 2^-24 < 2^-13) and a few roundings and exponentials a term
+    want = 1.75 * group * (lens > 0)
+    assert np.abs(sums - want[:, None]).max() <= 1.75 * group * 2.0 ** -10
+    assert pkv_check()[0] == 0
